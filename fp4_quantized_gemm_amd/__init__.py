@@ -19,6 +19,10 @@ trainer-side W4A16 product,
     grouped_w4a16_gemm
 and the FP8 (E4M3) W8A8 baseline the method is compared with,
     fp8_quantize, grouped_fp8_gemm
+and the training step around the W4A16 product: 8-bit activation checkpoints,
+the product's input and weight gradients, the SwiGLU's backward pass,
+    mxfp8_checkpoint, mxfp8_restore, grouped_w4a16_dgrad, grouped_wgrad,
+    moe_swiglu_backward
 """
 from __future__ import annotations
 
@@ -35,8 +39,9 @@ __all__ = ["lib", "nvfp4_qdq_weights", "nvfp4_pack_weights", "QdqWeights",
            "moe_permute", "grouped_w4a4_gemm_rac", "moe_unpermute_combine", "nvfp4_qdq_residual",
            "grouped_w4a16_gemm", "select_residual_channels_per_expert",
            "grouped_w4a4_gemm_rac_per_expert", "grouped_w4a4_gemm_rac_swiglu",
-           "nvfp4_quantize_act_amax", "fp8_quantize", "grouped_fp8_gemm", "NvfpError",
-           "EXPORTED_SYMBOLS"]
+           "nvfp4_quantize_act_amax", "fp8_quantize", "grouped_fp8_gemm",
+           "mxfp8_checkpoint", "mxfp8_restore", "grouped_w4a16_dgrad", "grouped_wgrad",
+           "moe_swiglu_backward", "NvfpError", "EXPORTED_SYMBOLS"]
 
 EXPORTED_SYMBOLS = [
     "nvfp4_version", "nvfp4_status_str", "nvfp4_last_error",
@@ -55,6 +60,10 @@ EXPORTED_SYMBOLS = [
     "nvfp4_quantize_act_amax",
     "fp8_quantize_workspace_size", "fp8_quantize",
     "grouped_fp8_gemm_workspace_size", "grouped_fp8_gemm",
+    "mxfp8_checkpoint", "mxfp8_restore",
+    "grouped_w4a16_dgrad_workspace_size", "grouped_w4a16_dgrad",
+    "grouped_wgrad_workspace_size", "grouped_wgrad",
+    "moe_swiglu_backward",
 ]
 
 
@@ -96,6 +105,8 @@ def _load():
         "grouped_w4a4_gemm_rac_swiglu_workspace_size": [_I64, _I64, _I64, _I64, _I64, _I64],
         "fp8_quantize_workspace_size": [_I64],
         "grouped_fp8_gemm_workspace_size": [_I64],
+        "grouped_w4a16_dgrad_workspace_size": [_I64, _I64, _I64, _I64],
+        "grouped_wgrad_workspace_size": [_I64, _I64, _I64, _I64],
     }.items():
         f = getattr(L, name)
         f.restype = _SZ
@@ -123,6 +134,13 @@ def _load():
         "nvfp4_quantize_act_amax": [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P],
         "fp8_quantize": [_P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P],
         "grouped_fp8_gemm": [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P],
+        "mxfp8_checkpoint": [_P, _I64, _I64, _I64, _P, _P, _P, _P],
+        "mxfp8_restore": [_P, _P, _I64, _I64, _P, _I64, _P],
+        "grouped_w4a16_dgrad": [_P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _SZ,
+                                _P],
+        "grouped_wgrad": [_P, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _P,
+                          ctypes.c_int, ctypes.c_int, _P, _SZ, _P],
+        "moe_swiglu_backward": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P],
     }
     for name, args in sigs.items():
         f = getattr(L, name)
@@ -181,6 +199,45 @@ def _need(t, dtype, name):
         raise NvfpError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise NvfpError(f"{name} must be contiguous")
+
+
+def _arg(t, dtype, name, dev, shape=None, optional=False, strided=False):
+    """Check one tensor argument: on dev, of the dtype, of the shape (None
+    entries are free), contiguous (strided: rows may be padded)."""
+    if t is None:
+        if optional:
+            return
+        raise NvfpError(f"{name} is required")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise NvfpError(f"{name} must be a device tensor")
+    if t.device != dev:
+        raise NvfpError(f"{name} is on {t.device}, the call is on {dev}")
+    if t.dtype != dtype:
+        raise NvfpError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
+        raise NvfpError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if strided:
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
+                (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise NvfpError(f"{name} must have contiguous rows")
+    elif not t.is_contiguous():
+        raise NvfpError(f"{name} must be contiguous")
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor with contiguous rows (one row: its width)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _call(name, dev, *args):
+    """One library call on dev's current stream, with dev the current device."""
+    fn = getattr(_load(), name)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), name)
 
 
 class QdqWeights(NamedTuple):
@@ -516,3 +573,136 @@ def moe_unpermute_combine(y, inv_perm, topk_w, out=None):
                                    _stream(y.device)),
            "moe_unpermute_combine")
     return o
+
+
+def mxfp8_checkpoint(x, glu=False, want_codes=True):
+    """8-bit checkpoint of x [M][K] bf16 (rows may be strided) -> dict(codes
+    [M][K] u8 E4M3, scales [M][K/32] u8 E8M0, h).  glu=True: x = [gate | up]
+    and h [M][K/2] bf16 = silu(gate) * up from the same read; h is None
+    otherwise.  want_codes=False (with glu): h alone."""
+    _arg(x, torch.bfloat16, "x", getattr(x, "device", None), (None, None), strided=True)
+    M, K = x.shape
+    dev = x.device
+    codes = scales = h = None
+    if want_codes:
+        codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+    if glu:
+        h = torch.empty((M, K // 2), dtype=torch.bfloat16, device=dev)
+    _call("mxfp8_checkpoint", dev, _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _ptr(h))
+    return dict(codes=codes, scales=scales, h=h)
+
+
+def mxfp8_restore(codes, scales, out=None):
+    """The bf16 values [M][K] that a checkpoint's codes and scales stand for
+    (exact).  out: a bf16 tensor to write, whose rows may be strided."""
+    dev = getattr(codes, "device", None)
+    _arg(codes, torch.uint8, "codes", dev, (None, None))
+    M, K = codes.shape
+    _arg(scales, torch.uint8, "scales", dev, (M, K // 32))
+    _arg(out, torch.bfloat16, "out", dev, (M, K), optional=True, strided=True)
+    x = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    _call("mxfp8_restore", dev, _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x))
+    return x
+
+
+def _m_total(M_total, *row_lists):
+    """Rows of the permuted side: as given, else a row list's length."""
+    for rows in row_lists:
+        if M_total is None and rows is not None:
+            M_total = int(rows.numel())
+    for rows in row_lists:
+        if rows is not None and rows.numel() < M_total:
+            raise NvfpError("a row list is shorter than M_total")
+    return M_total
+
+
+def grouped_w4a16_dgrad(dy, dy_rows, w_codes, w_scales, g_w, expert_offsets, M_total=None,
+                        out=None):
+    """dX [M_total][K] bf16 = dy (bf16 [M_src][N], gathered by dy_rows) times
+    the dequantized NVFP4 weights of each row's expert, contracted over N: the
+    input gradient of grouped_w4a16_gemm.  Rows outside the experts' are left
+    as they were."""
+    dev = getattr(dy, "device", None)
+    _arg(dy, torch.bfloat16, "dy", dev, (None, None))
+    M_src = dy.shape[0]
+    E, N = _wshape(w_codes)
+    K = int(w_codes.shape[3]) * 64
+    _arg(dy, torch.bfloat16, "dy", dev, (None, N))
+    _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
+    _arg(w_codes, torch.uint8, "w_codes", dev)
+    _arg(w_scales, torch.uint8, "w_scales", dev, (E, 2, N // 16, K // 64, 16, 4))
+    _arg(g_w, torch.float32, "g_w", dev, (E,))
+    _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
+    M_total = _m_total(M_total, dy_rows)
+    if M_total is None:
+        M_total = M_src
+    _arg(out, torch.bfloat16, "out", dev, (M_total, K), optional=True)
+    dx = out if out is not None else torch.empty((M_total, K), dtype=torch.bfloat16, device=dev)
+    ws = _ws(_load().grouped_w4a16_dgrad_workspace_size(E, M_total, N, K), dev)
+    _call("grouped_w4a16_dgrad", dev, _ptr(dy), _ptr(dy_rows), M_src, _ptr(w_codes),
+          _ptr(w_scales), _ptr(g_w), _ptr(expert_offsets), E, M_total, N, K, _ptr(dx), _ptr(ws),
+          ws.numel())
+    return dx
+
+
+def grouped_wgrad(dy, dy_rows, x, x_rows, expert_offsets, x_scales=None, M_total=None,
+                  dtype=torch.float32, out=None, accumulate=False):
+    """dW [E][N][K] = for each expert, dy^T x over its rows (dy [M_dy][N] bf16
+    gathered by dy_rows; x [M_x][K] bf16, or a checkpoint's codes with
+    x_scales, gathered by x_rows).  dtype float32 or bfloat16; out: a tensor
+    to write, with accumulate=True (float32) to add to."""
+    dev = getattr(dy, "device", None)
+    _arg(dy, torch.bfloat16, "dy", dev, (None, None))
+    _arg(x, torch.bfloat16 if x_scales is None else torch.uint8, "x", dev, (None, None))
+    (M_dy, N), (M_x, K) = dy.shape, x.shape
+    _arg(x_scales, torch.uint8, "x_scales", dev, (M_x, K // 32), optional=True)
+    _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
+    _arg(x_rows, torch.int32, "x_rows", dev, (None,), optional=True)
+    _arg(expert_offsets, torch.int32, "expert_offsets", dev, (None,))
+    E = int(expert_offsets.numel()) - 1
+    M_total = _m_total(M_total, dy_rows, x_rows)
+    if M_total is None:
+        M_total = min(M_dy, M_x)
+    if out is not None:
+        dtype = out.dtype
+    elif accumulate:
+        raise NvfpError("accumulate needs out")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise NvfpError(f"dw must be float32 or bfloat16, not {dtype}")
+    _arg(out, dtype, "out", dev, (E, N, K), optional=True)
+    dw = out if out is not None else torch.empty((E, N, K), dtype=dtype, device=dev)
+    ws = _ws(_load().grouped_wgrad_workspace_size(E, M_total, N, K), dev)
+    _call("grouped_wgrad", dev, _ptr(dy), _ptr(dy_rows), M_dy, _ptr(x), _ptr(x_scales),
+          _ptr(x_rows), M_x, _ptr(expert_offsets), E, M_total, N, K, _ptr(dw),
+          int(dtype == torch.bfloat16), int(bool(accumulate)), _ptr(ws), ws.numel())
+    return dw
+
+
+def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h=True):
+    """Backward of h = silu(gate) * up with the routing weights -> (dy
+    [P][2I] bf16, hw [P][I] bf16 = routing weight times h (None with
+    want_h=False), d_topk_w [T][tk] f32 (None without topk_w)).  y [P][2I] =
+    [gate | up] bf16, or a checkpoint's codes with y_scales; dh [P][I] bf16 is
+    h's gradient without the routing weight; inv_perm [T][tk] i32 and topk_w
+    [T][tk] f32 as moe_permute returns them (both None: one slot per row,
+    weight 1)."""
+    dev = getattr(y, "device", None)
+    _arg(y, torch.bfloat16 if y_scales is None else torch.uint8, "y", dev, (None, None))
+    P, I2 = y.shape
+    I = I2 // 2
+    if I2 != 2 * I:
+        raise NvfpError("y must be [gate | up]")
+    _arg(y_scales, torch.uint8, "y_scales", dev, (P, I2 // 32), optional=True)
+    _arg(dh, torch.bfloat16, "dh", dev, (P, I))
+    _arg(inv_perm, torch.int32, "inv_perm", dev, (None, None), optional=True)
+    T, tk = (P, 1) if inv_perm is None else inv_perm.shape
+    if T * tk != P:
+        raise NvfpError(f"inv_perm must have one entry for each of the {P} rows")
+    _arg(topk_w, torch.float32, "topk_w", dev, (T, tk), optional=True)
+    dy = torch.empty((P, I2), dtype=torch.bfloat16, device=dev)
+    hw = torch.empty((P, I), dtype=torch.bfloat16, device=dev) if want_h else None
+    dw = torch.empty((T, tk), dtype=torch.float32, device=dev) if topk_w is not None else None
+    _call("moe_swiglu_backward", dev, _ptr(y), _ptr(y_scales), _ptr(dh), _ptr(inv_perm),
+          _ptr(topk_w), T, tk, I, _ptr(dy), _ptr(hw), _ptr(dw))
+    return dy, hw, dw

@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "device.h"
+#include "mfma.h"
 #include "runtime.h"
 
 namespace nvfp4 {
@@ -92,11 +93,9 @@ k_tile_prefix(const int32_t* __restrict__ offsets, int E, int64_t M_total, int b
   if (tid == E - 1) prefix[E] = base + incl;
 }
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f32x4_t mfma_bf16(const u32x4& a, const u32x4& b, f32x4_t c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+void tile_prefix(const int32_t* offsets, int E, int64_t M_total, int bm, int32_t* prefix,
+                 hipStream_t s) {
+  k_tile_prefix<<<1, 1024, 0, s>>>(offsets, E, M_total, bm, prefix);
 }
 
 __global__ void __launch_bounds__(256)
@@ -317,7 +316,6 @@ constexpr int WS_BYTES = BN * WSROW > OUT_ROWS * OUTROW ? BN * WSROW : OUT_ROWS 
 
 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 template <int SEL>
 __device__ __forceinline__ uint32_t dec2_f16(uint32_t w, float sc, h2_t mu) {
@@ -339,20 +337,9 @@ __device__ __forceinline__ void scale_prep(uint32_t byte, float& sc, h2_t& mu) {
   sc = s;
 }
 
-__device__ __forceinline__ void wait_vmem0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// word 3 of a raw (untyped, stride 0) buffer resource on gfx9: 32-bit data
-// format, so dword loads return the bytes as stored
-constexpr int kBufferRsrcWord3 = 0x00020000;
-typedef __attribute__((address_space(3))) void* lds_void_ptr;
-__device__ __forceinline__ lds_void_ptr lds_ptr(void* p) { return (lds_void_ptr)p; }
 __device__ __forceinline__ f32x16_t mfma32_f16(const u32x4& a, const u32x4& b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
                                                 __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16_t mfma32_bf16(const u32x4& a, const u32x4& b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
-                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // codes [M][K/2] + scales [M][K/16] -> f16 image [M][K]; one thread per 8

@@ -1,0 +1,32 @@
+// Matrix-core and LDS-load helpers shared by the GEMM sources (gfx950 only).
+#pragma once
+#include "device.h"
+
+namespace nvfp4 {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x4_t mfma_bf16(const u32x4& a, const u32x4& b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma32_bf16(const u32x4& a, const u32x4& b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void wait_vmem0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// word 3 of a raw (untyped, stride 0) buffer resource on gfx9: 32-bit data
+// format, so dword loads return the bytes as stored
+constexpr int kBufferRsrcWord3 = 0x00020000;
+typedef __attribute__((address_space(3))) void* lds_void_ptr;
+__device__ __forceinline__ lds_void_ptr lds_ptr(void* p) { return (lds_void_ptr)p; }
+
+// prefix[e] = number of bm-row tiles of the experts before e, prefix[E] = of
+// all of them (one workgroup; E <= 1024); defined in gemm.hip
+void tile_prefix(const int32_t* offsets, int E, int64_t M_total, int bm, int32_t* prefix,
+                 hipStream_t s);
+
+}  // namespace nvfp4

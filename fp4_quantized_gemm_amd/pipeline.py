@@ -7,6 +7,10 @@ back, forms and quantizes the SwiGLU activation for the down projection the
 same way, and combines the expert outputs (QUADS: arXiv abstract;
 gist.science technical summary §2.1-§2.2).  Nothing here computes: every
 step is one call into libnvfp4rac.
+
+The trainer's side of the same block (asymmetric W4A16 QAT, summary §2.2 A):
+moe_train_forward keeps what the backward pass needs, by default in 8 bits,
+and moe_train_backward returns the gradients.
 """
 from __future__ import annotations
 
@@ -14,8 +18,9 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (grouped_w4a4_gemm_rac, grouped_w4a4_gemm_rac_per_expert,
-               grouped_w4a4_gemm_rac_swiglu, moe_permute, nvfp4_quantize_act_amax,
+from . import (grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
+               grouped_w4a4_gemm_rac_per_expert, grouped_w4a4_gemm_rac_swiglu, grouped_wgrad,
+               moe_permute, moe_swiglu_backward, mxfp8_checkpoint, nvfp4_quantize_act_amax,
                moe_unpermute_combine, nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act,
                select_residual_channels, select_residual_channels_per_expert)
 
@@ -102,3 +107,67 @@ def moe_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, k_
     if keep:
         out.update(y2=y2, st2=st2, out=o)
     return o, out
+
+
+@dataclass
+class TrainState:
+    """What moe_train_forward keeps for moe_train_backward."""
+    x: torch.Tensor          # the block's input: bf16, or its checkpoint's codes
+    x_scales: torch.Tensor   # ... and scales (None: bf16)
+    y1: torch.Tensor         # [gate | up] products by permuted row, likewise
+    y1_scales: torch.Tensor
+    topk_ids: torch.Tensor
+    topk_w: torch.Tensor
+    offsets: torch.Tensor
+    perm_token: torch.Tensor
+    inv_perm: torch.Tensor
+    w_first: QuantWeights
+    w_down: QuantWeights
+
+
+def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, bias=None,
+                      checkpoint="mxfp8"):
+    """The block with the trainer's W4A16 products (bf16 activations): x [T][H]
+    bf16, logits [T][E] f32, w_first [E][2I][H], w_down [E][H][I] -> (out
+    [T][H] bf16, TrainState).  checkpoint="mxfp8" keeps x and the gate and up
+    products in 8 bits (2.06 bytes per element of both together instead of 4),
+    "bf16" keeps them as they are."""
+    if checkpoint not in ("mxfp8", "bf16"):
+        raise ValueError(f"checkpoint must be 'mxfp8' or 'bf16', not {checkpoint!r}")
+    mx = checkpoint == "mxfp8"
+    ids, tw, offs, perm, inv = moe_permute(logits, topk, bias)
+    rows = perm.numel()
+    y1 = grouped_w4a16_gemm(x, perm, w_first.packed_codes, w_first.packed_scales, w_first.g, offs,
+                            M_total=rows)
+    c1 = mxfp8_checkpoint(y1, glu=True, want_codes=mx)
+    y2 = grouped_w4a16_gemm(c1["h"], None, w_down.packed_codes, w_down.packed_scales, w_down.g,
+                            offs, M_total=rows)
+    out = moe_unpermute_combine(y2, inv, tw)
+    kept_x, x_scales, kept_y, y_scales = x, None, y1, None
+    if mx:
+        c0 = mxfp8_checkpoint(x)
+        kept_x, x_scales, kept_y, y_scales = c0["codes"], c0["scales"], c1["codes"], c1["scales"]
+    return out, TrainState(kept_x, x_scales, kept_y, y_scales, ids, tw, offs, perm, inv, w_first,
+                           w_down)
+
+
+def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=None, dw_down=None):
+    """Gradients of moe_train_forward for d_out [T][H] bf16 -> dict(dx [T][H]
+    bf16, dw_first [E][2I][H], dw_down [E][H][I] (dw_dtype float32 or
+    bfloat16), d_topk_w [T][tk] f32).  dw_first, dw_down: float32 tensors that
+    the weight gradients are added to (gradient accumulation).  The routing
+    weight enters in the SwiGLU's backward pass, so d_out goes into both of the
+    down projection's products as it is, gathered by token."""
+    acc1, acc2 = dw_first is not None, dw_down is not None
+    rows = st.perm_token.numel()
+    dh = grouped_w4a16_dgrad(d_out, st.perm_token, st.w_down.packed_codes, st.w_down.packed_scales,
+                             st.w_down.g, st.offsets, M_total=rows)
+    dy1, hw, d_tw = moe_swiglu_backward(st.y1, dh, st.inv_perm, st.topk_w, y_scales=st.y1_scales)
+    g_down = grouped_wgrad(d_out, st.perm_token, hw, None, st.offsets, M_total=rows,
+                           dtype=dw_dtype, out=dw_down, accumulate=acc2)
+    g_first = grouped_wgrad(dy1, None, st.x, st.perm_token, st.offsets, x_scales=st.x_scales,
+                            M_total=rows, dtype=dw_dtype, out=dw_first, accumulate=acc1)
+    dxp = grouped_w4a16_dgrad(dy1, None, st.w_first.packed_codes, st.w_first.packed_scales,
+                              st.w_first.g, st.offsets, M_total=rows)
+    dx = moe_unpermute_combine(dxp, st.inv_perm, torch.ones_like(st.topk_w))
+    return dict(dx=dx, dw_first=g_first, dw_down=g_down, d_topk_w=d_tw)

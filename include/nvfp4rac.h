@@ -382,6 +382,88 @@ int grouped_fp8_gemm(const uint8_t* a, const float* g_x, const int32_t* a_rows, 
                      int64_t M_total, int64_t N, int64_t K, void* y, void* ws, size_t ws_bytes,
                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training step around the W4A16 product (asymmetric W4A16 QAT, gist.science
+ * summary §2.2 A): activations kept in 8 bits, the two gradients of the
+ * product, and the backward pass of the SwiGLU.  The pages describe the
+ * forward only; these are its plain derivatives, with the straight-through
+ * gradient for the weights (the gradient of W~ is taken as the master
+ * weight's).
+ *
+ * 8-bit activation checkpoints, OCP MXFP8: E4M3 codes [M][K] and one E8M0
+ * byte (2^(byte - 127)) per 32 consecutive elements of a row, [M][K/32].  The
+ * scale is the smallest power of two, at least 2^-117, that keeps the block's
+ * largest finite magnitude at or below 448 times it, so no code saturates; the
+ * code is E4M3(x / scale), round to nearest even (240 where that would stand
+ * for 2^128, which bf16 does not hold).  NaN and infinities get the NaN code
+ * (and the rest of their block its own scale).
+ *
+ * mxfp8_checkpoint: x [M][K] bf16, row stride ldx elements, is written as
+ *   codes and scales (both or neither NULL).  h [M][K/2] bf16 or NULL: with
+ *   x = [gate | up], h = bf16(silu(gate) * up) from the same read (the same
+ *   bits as nvfp4_quantize_act with glu = 1); codes NULL: h alone.
+ *   Requires M >= 0, K % 32 == 0 (K % 64 == 0 with h), ldx % 8 == 0;
+ *   codes 8-byte, scales unaligned, x and h 16-byte aligned.  No workspace.
+ * mxfp8_restore: x [M][K] bf16 (row stride ldx) = code * scale, exactly, for
+ *   codes and scales that mxfp8_checkpoint wrote.  No workspace.
+ * ---------------------------------------------------------------------- */
+int mxfp8_checkpoint(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
+                     uint8_t* scales, void* h, void* stream);
+int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* x,
+                  int64_t ldx, void* stream);
+
+/* Input gradient of grouped_w4a16_gemm.  dy [M_src][N] bf16; for row p of
+ * expert e, t = dy_rows ? dy_rows[p] : p:
+ *   dx[p][k] = bf16( g_w[e] * sum_n dy[t][n] * w~e[n][k] ),
+ * w~ = e2m1 * e4m3 exact in bf16, float32 accumulation, one rounding.  dx
+ * [M_total][K] bf16; rows outside [off[0], off[E]) are left as they were.
+ * The weights are the packed copy the forward takes.  Same rules for the
+ * expert grouping as grouped_w4a16_gemm.  Requires 1 <= E <= 1024,
+ * M_total < 2^31, N % 16 == 0, K % 64 == 0, M_src * N * 2 < 2^32,
+ * N * K / 2 < 2^32; dy_rows == NULL needs M_src >= M_total. */
+size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
+int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
+                        const uint8_t* w_codes, const uint8_t* w_scales, const float* g_w,
+                        const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N,
+                        int64_t K, void* dx, void* ws, size_t ws_bytes, void* stream);
+
+/* Weight gradient of the expert product, contracted over each expert's rows:
+ *   dw[e][n][k] = sum over p in [off[e], off[e+1]) of dy[t_p][n] * x[u_p][k],
+ * t_p = dy_rows ? dy_rows[p] : p, u_p = x_rows ? x_rows[p] : p.  dy [M_dy][N]
+ * bf16; x [M_x][K] bf16 (x_scales NULL), or the E4M3 codes of a checkpoint
+ * with its scales x_scales [M_x][K/32], multiplied as the exact bf16 values
+ * they stand for.  Float32 accumulation in an order that does not depend on
+ * timing.  dw [E][N][K]: float32, or bf16 with dw_bf16 = 1 (one rounding); an
+ * expert without rows gets zeros.  accumulate = 1 (float32 only): the sum is
+ * added to what dw holds.  Requires 1 <= E <= 1024, M_total < 2^31,
+ * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), M_dy * N * 2 < 2^32,
+ * x below 4 GiB; an operand without a row list has at least M_total rows. */
+size_t grouped_wgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
+int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const void* x,
+                  const uint8_t* x_scales, const int32_t* x_rows, int64_t M_x,
+                  const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                  void* dw, int dw_bf16, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward pass of h = silu(gate) * up with the routing weight of its row.
+ * Slot (t, j) of T tokens x tk slots is row p = inv_perm[t][j] (inv_perm NULL
+ * with tk = 1: p = t) with weight w = topk_w[t][j] (topk_w NULL: 1).
+ * y [T*tk][2I] = [gate | up] bf16, or the codes of its checkpoint with
+ * y_scales [T*tk][2I/32]; dh [T*tk][I] bf16, the gradient of h with the
+ * routing weight left out (the input gradient of the down product, of
+ * d_out[t] itself).  With s = 1 / (1 + e^-gate), in float32:
+ *   dy[p] = [ w dh up s (1 + gate (1 - s)) | w dh gate s ]   bf16 [T*tk][2I]
+ *   hw[p] = w gate s up                  bf16 [T*tk][I] or NULL (the x of the
+ *           down product's grouped_wgrad, whose dy is d_out itself)
+ *   d_topk_w[t][j] = sum_i dh_i gate_i s_i up_i   float32 [T][tk] or NULL
+ * The gradient of the routing logits follows from d_topk_w as that of a
+ * softmax over the tk chosen experts.  inv_perm is a permutation; an entry
+ * outside [0, T*tk) is skipped.  Requires 1 <= tk <= 32, T*tk < 2^31,
+ * I % 8 == 0 (I % 32 == 0 with y_scales); y (8-byte with y_scales), dh, dy and
+ * hw 16-byte aligned.  No workspace. */
+int moe_swiglu_backward(const void* y, const uint8_t* y_scales, const void* dh,
+                        const int32_t* inv_perm, const float* topk_w, int64_t T, int64_t tk,
+                        int64_t I, void* dy, void* hw, float* d_topk_w, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,9 +16,11 @@ Modules:
   layer    the whole MoE layer chained from the pieces above
   fp8      the FP8 (E4M3) W8A8 baseline: per-tensor quantization and the
            expert-grouped product
+  train    8-bit activation checkpoints, the gradients of the W4A16 product
+           and of the SwiGLU with its routing weights
 
 Every function is pinned by tests under tests/ against facts that do not come
 from the oracle itself (bit definitions, exact rational arithmetic, library
 routines, closed forms and invariants).
 """
-from . import formats, fp8, gemm, layer, moe, nvfp4  # noqa: F401
+from . import formats, fp8, gemm, layer, moe, nvfp4, train  # noqa: F401

@@ -1,0 +1,119 @@
+"""Refusals of the training-step calls, on the CPU: every call below fails its
+argument checks before it touches memory or launches anything."""
+import ctypes
+
+import pytest
+import torch
+
+import fp4_quantized_gemm_amd as F
+
+OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_WS, ERR_UNSUP = 0, 1, 2, 3, 4, 5
+A = ctypes.c_void_p(0x10000)
+MIS = ctypes.c_void_p(0x10002)
+
+
+def test_checkpoint_refusals():
+    L = F.lib()
+    ck = L.mxfp8_checkpoint
+    assert ck(A, 4, 48, 48, A, A, None, None) == ERR_SHAPE           # K % 32
+    assert ck(A, 4, 0, 0, A, A, None, None) == ERR_SHAPE
+    assert ck(A, -1, 64, 64, A, A, None, None) == ERR_SHAPE
+    assert ck(A, 4, 64, 56, A, A, None, None) == ERR_SHAPE           # ldx < K
+    assert ck(A, 4, 64, 68, A, A, None, None) == ERR_SHAPE           # ldx % 8
+    assert ck(A, 4, 96, 96, A, A, A, None) == ERR_SHAPE              # h needs K % 64
+    assert ck(A, 4, 64, 64, A, None, None, None) == ERR_NULL
+    assert ck(A, 4, 64, 64, None, None, None, None) == ERR_NULL
+    assert ck(None, 4, 64, 64, A, A, None, None) == ERR_NULL
+    assert ck(MIS, 4, 64, 64, A, A, None, None) == ERR_ALIGN
+    assert ck(A, 4, 64, 64, MIS, A, None, None) == ERR_ALIGN
+    assert ck(None, 0, 64, 64, A, A, None, None) == OK
+    rs = L.mxfp8_restore
+    assert rs(A, A, 4, 40, A, 40, None) == ERR_SHAPE
+    assert rs(A, A, 4, 64, A, 32, None) == ERR_SHAPE
+    assert rs(A, None, 4, 64, A, 64, None) == ERR_NULL
+    assert rs(A, A, 4, 64, MIS, 64, None) == ERR_ALIGN
+    assert rs(None, None, 0, 64, None, 64, None) == OK
+
+
+def dgrad(dy=A, rows=A, M=64, wc=A, ws=A, g=A, off=A, E=2, P=128, N=64, K=128, dx=A, w=A,
+          wb=1 << 30):
+    return F.lib().grouped_w4a16_dgrad(dy, rows, M, wc, ws, g, off, E, P, N, K, dx, w, wb, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(E=0), ERR_SHAPE), (dict(E=1025), ERR_SHAPE), (dict(N=24), ERR_SHAPE),
+    (dict(K=96), ERR_SHAPE), (dict(P=-1), ERR_SHAPE), (dict(P=1 << 31), ERR_SHAPE),
+    (dict(rows=None), ERR_SHAPE),                       # 64 rows for 128
+    (dict(M=0), ERR_SHAPE), (dict(M=-3), ERR_SHAPE),
+    (dict(M=1 << 26), ERR_UNSUP),                       # dy of 8 GiB
+    (dict(dy=None), ERR_NULL), (dict(wc=None), ERR_NULL), (dict(ws=None), ERR_NULL),
+    (dict(g=None), ERR_NULL), (dict(off=None), ERR_NULL), (dict(dx=None), ERR_NULL),
+    (dict(w=None), ERR_NULL), (dict(dy=MIS), ERR_ALIGN), (dict(dx=MIS), ERR_ALIGN),
+    (dict(wc=MIS), ERR_ALIGN), (dict(wb=4), ERR_WS), (dict(P=0, M=0), OK),
+])
+def test_dgrad_refusals(kw, want):
+    assert dgrad(**kw) == want
+    if want != OK:
+        assert b"grouped_w4a16_dgrad" in F.lib().nvfp4_last_error()
+
+
+def wgrad(dy=A, dyr=None, Md=128, x=A, xs=None, xr=None, Mx=128, off=A, E=2, P=128, N=64, K=64,
+          dw=A, bf=0, acc=0, w=A, wb=1 << 30):
+    return F.lib().grouped_wgrad(dy, dyr, Md, x, xs, xr, Mx, off, E, P, N, K, dw, bf, acc, w, wb,
+                                 None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(E=0), ERR_SHAPE), (dict(E=1025), ERR_SHAPE), (dict(N=12), ERR_SHAPE),
+    (dict(K=4), ERR_SHAPE), (dict(K=40, xs=A), ERR_SHAPE), (dict(P=-1), ERR_SHAPE),
+    (dict(Md=127), ERR_SHAPE), (dict(Mx=127), ERR_SHAPE),
+    (dict(Md=0, dyr=A), ERR_SHAPE), (dict(Mx=0, xr=A), ERR_SHAPE),
+    (dict(Md=1 << 25), ERR_UNSUP), (dict(Mx=1 << 25), ERR_UNSUP),
+    (dict(Mx=1 << 26, xs=A), ERR_UNSUP),
+    (dict(bf=2), ERR_UNSUP), (dict(bf=1, acc=1), ERR_UNSUP),
+    (dict(dy=None), ERR_NULL), (dict(x=None), ERR_NULL), (dict(off=None), ERR_NULL),
+    (dict(dw=None), ERR_NULL), (dict(w=None), ERR_NULL),
+    (dict(dy=MIS), ERR_ALIGN), (dict(x=MIS), ERR_ALIGN), (dict(dw=MIS), ERR_ALIGN),
+    (dict(wb=8), ERR_WS),
+])
+def test_wgrad_refusals(kw, want):
+    assert wgrad(**kw) == want
+    assert b"grouped_wgrad" in F.lib().nvfp4_last_error()
+
+
+def swiglu(y=A, ys=None, dh=A, inv=A, w=A, T=8, tk=2, I=64, dy=A, hw=A, dw=A):
+    return F.lib().moe_swiglu_backward(y, ys, dh, inv, w, T, tk, I, dy, hw, dw, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), ERR_SHAPE), (dict(tk=0), ERR_SHAPE), (dict(tk=33), ERR_SHAPE),
+    (dict(I=12), ERR_SHAPE), (dict(I=40, ys=A), ERR_SHAPE), (dict(T=1 << 30), ERR_SHAPE),
+    (dict(y=None), ERR_NULL), (dict(dh=None), ERR_NULL), (dict(dy=None), ERR_NULL),
+    (dict(w=None), ERR_NULL), (dict(inv=None), ERR_NULL),
+    (dict(y=MIS), ERR_ALIGN), (dict(dh=MIS), ERR_ALIGN), (dict(hw=MIS), ERR_ALIGN),
+    (dict(T=0), OK),
+])
+def test_swiglu_backward_refusals(kw, want):
+    assert swiglu(**kw) == want
+
+
+def test_workspace_queries_take_any_sizes():
+    L = F.lib()
+    for q in (L.grouped_w4a16_dgrad_workspace_size, L.grouped_wgrad_workspace_size):
+        assert q(128, 131072, 4096, 1536) > 0
+        assert q(0, -1, -1, -1) > 0
+
+
+def test_binding_refuses_host_tensors():
+    b = torch.zeros(4, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(F.NvfpError, match="device tensor"):
+        F.mxfp8_checkpoint(b)
+    with pytest.raises(F.NvfpError, match="device tensor"):
+        F.mxfp8_restore(b.view(torch.uint8), b.view(torch.uint8))
+    with pytest.raises(F.NvfpError, match="device tensor"):
+        F.grouped_wgrad(b, None, b, None, i)
+    with pytest.raises(F.NvfpError, match="device tensor"):
+        F.moe_swiglu_backward(b, b)
+    with pytest.raises(F.NvfpError, match="device tensor"):
+        F.grouped_w4a16_dgrad(b, None, b, b, b, i)
