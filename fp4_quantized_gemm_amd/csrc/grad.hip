@@ -3,7 +3,7 @@
 // technical summary §2.2 A): the input gradient, a product with the same NVFP4
 // weights contracted over their rows, and the weight gradient, contracted over
 // each expert's own rows (the straight-through gradient of the master weight).
-#include <cstring>
+#include <type_traits>
 
 #include "device.h"
 #include "mfma.h"
@@ -27,7 +27,9 @@ struct GradArgs {
   void* dw;                    // wgrad: [E][N][K] f32 or bf16
   int64_t M_dy, M_x, M_total, N, K;
   int E;
-  int dw_bf16, accumulate;
+  int accumulate;
+  int run;                     // wgrad: log2 of the tiles an XCD takes in a row
+  int nsplit;                  // wgrad: slices of the rows (blockIdx.y); dw holds their partials
 };
 
 __device__ __forceinline__ void expert_rows(const GradArgs& p, int e, int64_t& lo, int64_t& hi) {
@@ -42,114 +44,396 @@ __device__ __forceinline__ int64_t source_row(const int32_t* rows, int64_t p, in
   return t < 0 ? 0 : (t >= M ? M - 1 : t);
 }
 
-// 64x64 outputs per workgroup, contraction 32 at a time; both operands in LDS
-// with the contraction contiguous.  DGRAD: outputs [rows][k], contraction n;
-// else outputs [n][k], contraction over the expert's rows.
-template <bool DGRAD>
-__global__ void __launch_bounds__(256)
-k_grad_simple(GradArgs p) {
-  __shared__ __attribute__((aligned(16))) uint16_t As[64][40];
-  __shared__ __attribute__((aligned(16))) uint16_t Bs[64][40];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t b0 = (int64_t)blockIdx.x * 64;
-  int e;
+// ---------------------------------------------------------------------------
+// 256x256 outputs per workgroup, eight waves (two rows of four, 128x64 each:
+// four by two 32x32 accumulators), contraction 64 at a time through two LDS
+// stages.  "Rows" are dx rows (kDgrad) or dw rows n; columns are k.
+//
+// An operand whose contraction index is its slow one (both of wgrad's, the
+// weights of dgrad) lies in LDS as it does in memory, [64][256] bf16, and is
+// read through the transposing LDS load: a group of 16 lanes reads 4
+// contraction rows of 16 columns and each lane gets its column's four values.
+// 16-byte chunk c of contraction row r sits at c ^ swz(r): the four rows of a
+// transposing load then lie in the four 64-byte parts of the 256-byte bank
+// line, and 16 rows of one chunk (the order in which decoded weights are
+// written) in 16 different 16-byte slots, so neither conflicts.
+// dgrad's dy has the contraction fast: [256][64], 16-byte fragment reads,
+// chunk c of row r at c ^ ((r >> 1) & 7).
+// bf16 operands go from memory to LDS directly; 4-bit weights and 8-bit
+// activations are decoded (exactly) on the way, once per workgroup.
+// ---------------------------------------------------------------------------
+namespace gr {
+constexpr int BM = 256, BN = 256, BC = 64;
+constexpr int A_BYTES = BM * BC * 2;
+constexpr int STAGE = A_BYTES + BN * BC * 2;   // 65536
+enum Mode { kDgrad, kWgrad, kWgradMx };
+}  // namespace gr
+
+// an offset past every buffer: such a load returns zeros
+constexpr uint32_t kPastBuffer = 0xFFFFFFF0u;
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t* lds_tr_ptr;
+
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+
+// 8 contraction values of one column: two transposing loads of 4 rows each
+__device__ __forceinline__ u32x4 tr_frag(const uint8_t* lo, const uint8_t* hi) {
+  const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_ptr)lo);
+  const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_tr_ptr)hi);
+  return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
+                                           kBufferRsrcWord3);
+}
+
+// MODE: which product.  BF16: the output is bf16, staged through LDS for
+// 16-byte row stores (the product is formed transposed, so that a lane holds
+// four consecutive columns); else float32, stored from the accumulators (32
+// lanes write 128 consecutive bytes).
+template <int MODE, bool BF16>
+__global__ void __launch_bounds__(512, 1)
+k_grad(GradArgs p, int n_tiles, int m_tiles) {
+  using namespace gr;
+  // two objects, and the loop unrolled by two: each access names its stage,
+  // so the fill of one stage is not waited for before reads of the other
+  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
+  __shared__ int32_t rows_src[MODE == kDgrad ? BM : 1];
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int kg = lane >> 5, r32 = lane & 31;
+
+  // tile order (workgroup b runs on XCD b % 8, each with its own L2)
+  int e, nt;
   int64_t lo, hi, a0;
-  if constexpr (DGRAD) {
-    const int gt = blockIdx.y;
-    if (gt >= p.prefix[p.E]) return;
-    int l = 0, h = p.E;
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (p.prefix[mid] <= gt) l = mid; else h = mid;
-    }
-    e = l;
-    expert_rows(p, e, lo, hi);
-    a0 = lo + (int64_t)(gt - p.prefix[e]) * 64;
-  } else {
-    e = blockIdx.z;
-    expert_rows(p, e, lo, hi);
-    a0 = (int64_t)blockIdx.y * 64;
-  }
-  f32x4_t acc[2][2] = {};
-  const int wa = (wave >> 1) * 32, wb = (wave & 1) * 32;
-  const int64_t c_end = DGRAD ? p.N : hi - lo;
-  for (int64_t c0 = 0; c0 < c_end; c0 += 32) {
-    u32x4 va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-    if constexpr (DGRAD) {
-      const int r = tid >> 2;
-      const int64_t pr = a0 + r, c = c0 + (tid & 3) * 8;
-      if (pr < hi && c < p.N)
-        va = *reinterpret_cast<const u32x4*>(p.dy + source_row(p.dy_rows, pr, p.M_dy) * p.N + c);
-      *reinterpret_cast<u32x4*>(&As[r][(tid & 3) * 8]) = va;
-      const int cc = tid >> 3;
-      const int64_t n = c0 + cc, k = b0 + (tid & 7) * 8;
-      if (n < p.N && k < p.K) {
-        const uint8_t* wc = p.w_codes + e * packed_codes_per_expert(p.N, p.K);
-        const uint8_t* ws = p.w_scales + e * packed_scales_per_expert(p.N, p.K);
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(wc + wcode_offset(n, k, p.K));
-        vb = decode8_bf16(w, e4m3_decode(ws[wscale_offset(n, k >> 4, p.K)]));
+  {
+    const int b = (int)blockIdx.x;
+    if constexpr (MODE == kDgrad) {
+      // groups of 4 row tiles x all column tiles, a contiguous range per XCD
+      const int real_m = p.prefix[p.E];
+      const int real_blocks = ((real_m + 3) / 4) * 4 * n_tiles;
+      const int per_xcd = (real_blocks + 7) / 8;
+      if ((b >> 3) >= per_xcd) return;
+      const int v = (b & 7) * per_xcd + (b >> 3);
+      if (v >= real_blocks) return;
+      const int group = 4 * n_tiles;
+      const int gi = v / group, g = v - gi * group;
+      const int gm = real_m - 4 * gi < 4 ? real_m - 4 * gi : 4;
+      const int gt = 4 * gi + g % gm;
+      nt = g / gm;
+      if (gt >= real_m || nt >= n_tiles) return;
+      int l = 0, h = p.E;
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (p.prefix[mid] <= gt) l = mid; else h = mid;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        Bs[(tid & 7) * 8 + i][cc] = (uint16_t)(vb[i >> 1] >> (16 * (i & 1)));
+      e = l;
+      expert_rows(p, e, lo, hi);
+      a0 = lo + (int64_t)(gt - p.prefix[e]) * BM;
     } else {
-      const int cc = tid >> 3, j = (tid & 7) * 8;
-      const int64_t pr = lo + c0 + cc, n = a0 + j, k = b0 + j;
-      if (pr < hi) {
-        if (n < p.N)
-          va = *reinterpret_cast<const u32x4*>(p.dy + source_row(p.dy_rows, pr, p.M_dy) * p.N + n);
-        if (k < p.K) {
-          const int64_t t = source_row(p.x_rows, pr, p.M_x);
-          if (p.x_scales)
-            vb = mx_decode8(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.x) +
-                                                            t * p.K + k),
-                            mx_scale(p.x_scales[t * (p.K / 32) + k / 32]));
-          else
-            vb = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + t * p.K + k);
+      // runs of 2^run tiles of an expert go to the XCDs in turn
+      const int per_e = n_tiles * m_tiles;
+      const int total = per_e * p.E;
+      const int loc = b >> 3, run = p.run;
+      const int v = ((((loc >> run) << 3) + (b & 7)) << run) + (loc & ((1 << run) - 1));
+      if (v >= total) return;
+      e = v / per_e;
+      const int t = v - e * per_e;
+      nt = t % n_tiles;
+      a0 = (int64_t)(t / n_tiles) * BM;
+      expert_rows(p, e, lo, hi);
+      if (p.nsplit > 1) {   // this slice's rows: whole steps
+        const int64_t steps = (hi - lo + BC - 1) / BC;
+        const int64_t per = (steps + p.nsplit - 1) / p.nsplit * BC;
+        const int64_t l = lo + per * blockIdx.y;
+        lo = l < hi ? l : hi;
+        hi = lo + per < hi ? lo + per : hi;
+      }
+    }
+  }
+  const int64_t b0 = (int64_t)nt * BN;
+  const int steps = MODE == kDgrad ? (int)((p.N + BC - 1) / BC) : (int)((hi - lo + BC - 1) / BC);
+
+  // ---- loads -------------------------------------------------------------
+  const uint32_t N2 = (uint32_t)(p.N * 2);
+  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * (uint64_t)p.N * 2);
+  // [64][256] tiles: lane's contraction row is 16 i + r16 of the step (i of
+  // four), its slot in the row lane % 32, which holds chunk tr_c
+  const int r16 = 2 * wave + kg;
+  const int tr_c = r32 ^ swz(r16);
+  uint32_t off_a[4];             // dgrad: byte offsets of the four loads at step 0
+  uint32_t col_a = 0, col_b = 0; // wgrad: byte offset of the lane's chunk in a row
+  int32_t row_a[4], row_b[4];    // wgrad: rows of the next loads (-1: none)
+  uint32_t chunk_n[4];           // dgrad: first column of the chunk
+  if constexpr (MODE == kDgrad) {
+    if (tid < BM) {
+      int64_t pr = a0 + tid;
+      if (pr >= hi) pr = hi - 1;
+      rows_src[tid] = (int32_t)source_row(p.dy_rows, pr, p.M_dy);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = (i * 8 + wave) * 64 + lane;
+      const int r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
+      off_a[i] = (uint32_t)rows_src[r] * N2 + 16u * c;
+      chunk_n[i] = 8u * c;
+    }
+  } else {
+    const int64_t n = a0 + 8 * tr_c, k = b0 + 8 * tr_c;
+    col_a = n < p.N ? (uint32_t)n * 2 : kPastBuffer;
+    col_b = k < p.K ? (uint32_t)k * (MODE == kWgrad ? 2 : 1) : kPastBuffer;
+  }
+  auto load_rows = [&](int step) __attribute__((always_inline)) {
+    if constexpr (MODE != kDgrad) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t pr = lo + (int64_t)step * BC + 16 * i + r16;
+        row_a[i] = row_b[i] = -1;
+        if (pr < hi) {
+          row_a[i] = (int32_t)source_row(p.dy_rows, pr, p.M_dy);
+          row_b[i] = (int32_t)source_row(p.x_rows, pr, p.M_x);
         }
       }
+    }
+  };
+  const uint64_t x_bytes = (uint64_t)p.M_x * (uint64_t)p.K * (MODE == kWgrad ? 2 : 1);
+  const __amdgpu_buffer_rsrc_t rs_b =
+      MODE == kDgrad ? buffer_of(p.w_codes + e * packed_codes_per_expert(p.N, p.K),
+                                 (uint64_t)p.N * p.K / 2)
+                     : buffer_of(p.x, x_bytes);
+  const __amdgpu_buffer_rsrc_t rs_s =
+      MODE == kDgrad ? buffer_of(p.w_scales + e * packed_scales_per_expert(p.N, p.K),
+                                 (uint64_t)p.N * p.K / 16)
+                     : buffer_of(p.x_scales, (uint64_t)p.M_x * (uint64_t)p.K / 32);
+  // dgrad weights: wave w takes the step's code tiles 2 w, 2 w + 1 (of 4 row
+  // blocks x 4 column tiles), lane l one row's half tile: 16 bytes = 32 k
+  const int w_rb = (2 * wave + kg) >> 2, w_ct = (2 * wave + kg) & 3;
+  const int w_half = (lane >> 4) & 1, w_row = lane & 15;
+  uint32_t off_w = 0, off_ws = 0;
+  const uint32_t w_step = (uint32_t)(4 * (p.K >> 6) * 512);
+  if constexpr (MODE == kDgrad) {
+    int64_t kt = (b0 >> 6) + w_ct;
+    if (kt >= (p.K >> 6)) kt = (p.K >> 6) - 1;   // columns past K are never stored
+    const uint32_t tile = (uint32_t)(w_rb * (p.K >> 6) + kt);
+    off_w = tile * 512 + w_half * 256 + w_row * 16;
+    off_ws = tile * 64 + w_row * 4 + w_half * 2;
+  }
+  u32x4 wreg;
+  uint32_t sreg[4];
+  uint32_t creg[4][2];
+
+  auto issue = [&](uint8_t* st, int step) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        As[j + i][cc] = (uint16_t)(va[i >> 1] >> (16 * (i & 1)));
-        Bs[j + i][cc] = (uint16_t)(vb[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 4; ++i) {
+      uint8_t* dst = st + (i * 8 + wave) * 1024;
+      if constexpr (MODE == kDgrad) {
+        const uint32_t n0 = (uint32_t)step * BC;
+        const uint32_t o = n0 + chunk_n[i] < (uint32_t)p.N ? off_a[i] : kPastBuffer;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, n0 * 2, 0, 0);
+      } else {
+        const uint32_t o = row_a[i] < 0 || col_a == kPastBuffer
+                               ? kPastBuffer : (uint32_t)row_a[i] * N2 + col_a;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, 0, 0, 0);
+        if constexpr (MODE == kWgrad) {
+          const uint32_t ob = row_b[i] < 0 || col_b == kPastBuffer
+                                  ? kPastBuffer : (uint32_t)row_b[i] * (uint32_t)(p.K * 2) + col_b;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, lds_ptr(dst + A_BYTES), 16, ob, 0, 0, 0);
+        } else {
+          const bool none = row_b[i] < 0 || col_b == kPastBuffer;
+          const uint32_t ob = none ? kPastBuffer : (uint32_t)row_b[i] * (uint32_t)p.K + col_b;
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_b, ob, 0, 0);
+          creg[i][0] = v[0];
+          creg[i][1] = v[1];
+          sreg[i] = __builtin_amdgcn_raw_buffer_load_b8(rs_s, none ? kPastBuffer : ob >> 5, 0, 0);
+        }
       }
     }
-    __syncthreads();
-    const int r = lane & 15, g = lane >> 4;
-    u32x4 fa[2], fb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fa[i] = *reinterpret_cast<const u32x4*>(&As[wa + 16 * i + r][8 * g]);
-      fb[i] = *reinterpret_cast<const u32x4*>(&Bs[wb + 16 * i + r][8 * g]);
+    if constexpr (MODE == kDgrad) {
+      const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs_b, off_w, (uint32_t)step * w_step, 0);
+      wreg = u32x4{v[0], v[1], v[2], v[3]};
+      sreg[0] = __builtin_amdgcn_raw_buffer_load_b16(rs_s, off_ws, (uint32_t)step * (w_step >> 3), 0);
     }
+    load_rows(step + 1);
+  };
+  // decode what issue() left in registers into the stage
+  auto fill = [&](uint8_t* st) __attribute__((always_inline)) {
+    if constexpr (MODE == kDgrad) {
+      const float s0 = e4m3_decode(sreg[0] & 0xFFu), s1 = e4m3_decode(sreg[0] >> 8);
+      const int r = 16 * w_rb + w_row;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j) {
+        const int c = 8 * w_ct + 4 * w_half + j;
+        *reinterpret_cast<u32x4*>(st + A_BYTES + r * 512 + ((c ^ swz(w_row)) << 4)) =
+            decode8_bf16(wreg[j], j < 2 ? s0 : s1);
+      }
+    } else if constexpr (MODE == kWgradMx) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(fa[i], fb[j], acc[i][j]);
-    __syncthreads();
-  }
-  const float sc = DGRAD ? p.g_w[e] : 1.0f;
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x4*>(st + A_BYTES + (i * 8 + wave) * 1024 + lane * 16) =
+            mx_decode8(make_uint2(creg[i][0], creg[i][1]), mx_scale(sreg[i]));
+    }
+  };
+
+  // ---- products ----------------------------------------------------------
+  f32x16_t acc[4][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t a = a0 + wa + 16 * i + 4 * (lane >> 4) + r;
-        const int64_t k = b0 + wb + 16 * j + (lane & 15);
-        if (k >= p.K || a >= (DGRAD ? hi : p.N)) continue;
-        if constexpr (DGRAD) {
-          p.dx[a * p.K + k] = (uint16_t)bf16x2_rne(acc[i][j][r] * sc, 0.f);
-        } else {
-          const int64_t at = ((int64_t)e * p.N + a) * p.K + k;
-          if (p.dw_bf16) {
-            static_cast<uint16_t*>(p.dw)[at] = (uint16_t)bf16x2_rne(acc[i][j][r], 0.f);
-          } else {
-            float* d = static_cast<float*>(p.dw) + at;
-            *d = p.accumulate ? *d + acc[i][j][r] : acc[i][j][r];
-          }
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // transposing loads: lane i of a 16-lane group g reads row 8 (g / 2) + 4 h
+  // + i / 4 of the 16-row slice, columns 16 (g % 2) + 4 (i % 4) .. + 3 of the
+  // fragment's 32 (4 chunks)
+  const int t_row = 8 * kg + ((lane & 15) >> 2);
+  const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const uint32_t t_off0 = t_row * 512 + ((t_chunk ^ swz(t_row)) << 4) + (lane & 1) * 8;
+  const uint32_t t_off1 = (t_row + 4) * 512 + ((t_chunk ^ swz(t_row + 4)) << 4) + (lane & 1) * 8;
+  // fragment f (32 columns = 4 chunks, 64 bytes): chunk bits 2.. are xored too
+  auto tr_at = [&](const uint8_t* t, int slice, int f) __attribute__((always_inline)) {
+    const uint32_t x = (uint32_t)f << 6;   // f < 8: bits 6..8 of the slot's byte offset
+    return tr_frag(t + slice * 8192 + (t_off0 ^ x), t + slice * 8192 + (t_off1 ^ x));
+  };
+  const int sw = (r32 >> 1) & 7;
+  auto compute = [&](const uint8_t* st, auto nv_c) __attribute__((always_inline)) {
+    constexpr int NV = decltype(nv_c)::value;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      u32x4 B[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) B[j] = tr_at(st + A_BYTES, s, 2 * wn + j);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        u32x4 A;
+        if constexpr (MODE == kDgrad)
+          A = *reinterpret_cast<const u32x4*>(st + (wm * 128 + 32 * i + r32) * 128 +
+                                              (((2 * s + kg) ^ sw) << 4));
+        else
+          A = tr_at(st, s, 4 * wm + i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = BF16 ? mfma32_bf16(B[j], A, acc[i][j]) : mfma32_bf16(A, B[j], acc[i][j]);
+      }
+    }
+  };
+  auto kstep = [&](const uint8_t* cur, uint8_t* nxt, int s, auto nv_c) __attribute__((always_inline)) {
+    if (s + 1 < steps) issue(nxt, s + 1);
+    compute(cur, nv_c);
+    if (s + 1 < steps) fill(nxt);
+    wait_vmem0();
+    __syncthreads();
+  };
+  auto run = [&](auto nv_c) __attribute__((always_inline)) {
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+      kstep(st0, st1, s, nv_c);
+      kstep(st1, st0, s + 1, nv_c);
+    }
+    if (s < steps) kstep(st0, st1, s, nv_c);
+  };
+  load_rows(0);
+  if (steps > 0) {
+    issue(st0, 0);
+    fill(st0);
+  }
+  wait_vmem0();
+  __syncthreads();
+  if constexpr (MODE == kDgrad) {
+    // rows of this wave inside the expert: only their 32-row blocks
+    const int64_t vr = hi - a0 - wm * 128;
+    if (vr > 64) run(std::integral_constant<int, 4>{});
+    else if (vr > 32) run(std::integral_constant<int, 2>{});
+    else if (vr > 0) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 0>{});
+  } else {
+    run(std::integral_constant<int, 4>{});
+  }
+
+  // ---- outputs -----------------------------------------------------------
+  const float sc = MODE == kDgrad ? p.g_w[e] : 1.0f;
+  if constexpr (BF16) {
+    // row 32 i + r32 of the wave's half tile, columns 64 wn + 32 j + 8 q +
+    // 4 kg .. + 3; 16-byte chunk c of row r at c ^ (r & 15)
+    uint8_t* half = wm ? st1 : st0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 32 * i + r32, c = 8 * wn + 4 * j + q;
+          const f32x16_t& v = acc[i][j];
+          *reinterpret_cast<uint2*>(half + r * 512 + ((c ^ (r & 15)) << 4) + kg * 8) =
+              make_uint2(bf16x2_rne(v[4 * q] * sc, v[4 * q + 1] * sc),
+                         bf16x2_rne(v[4 * q + 2] * sc, v[4 * q + 3] * sc));
+        }
+    __syncthreads();
+    const int64_t rows_end = MODE == kDgrad ? hi : p.N;
+    uint16_t* out = MODE == kDgrad ? p.dx
+                                   : static_cast<uint16_t*>(p.dw) + (int64_t)e * p.N * p.K;
+#pragma unroll 4
+    for (int q = tid; q < BM * 32; q += 512) {
+      const int r = q >> 5, c = q & 31;
+      const int64_t a = a0 + r, k = b0 + 8 * c;
+      const uint8_t* src = (r < 128 ? st0 : st1) + (r & 127) * 512 + ((c ^ (r & 15)) << 4);
+      if (a < rows_end && k < p.K)
+        *reinterpret_cast<uint4*>(out + a * p.K + k) = *reinterpret_cast<const uint4*>(src);
+    }
+  } else {
+    float* out = static_cast<float*>(p.dw) +
+                 ((int64_t)(p.nsplit > 1 ? blockIdx.y : 0) * p.E + e) * p.N * p.K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t k = b0 + 64 * wn + 32 * j + r32;
+        if (k >= p.K) continue;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t a = a0 + 128 * wm + 32 * i + 8 * (r >> 2) + 4 * kg + (r & 3);
+          if (a >= p.N) continue;
+          float* d = out + a * p.K + k;
+          *d = p.accumulate ? *d + acc[i][j][r] : acc[i][j][r];
         }
       }
+  }
+}
+
+// dw = sum of the slices' partial products, in slice order; 4 per lane
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+k_wgrad_reduce(const float* __restrict__ part, int64_t n, int nsplit, void* __restrict__ dw,
+               int accumulate) {
+  for (int64_t q = (blockIdx.x * 256LL + threadIdx.x) * 4; q < n; q += gridDim.x * 1024LL) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(part + q);
+    for (int i = 1; i < nsplit; ++i) s += *reinterpret_cast<const f32x4*>(part + i * n + q);
+    if constexpr (BF16) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dw) + q) =
+          make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
+    } else {
+      f32x4* d = reinterpret_cast<f32x4*>(static_cast<float*>(dw) + q);
+      *d = accumulate ? *d + s : s;
+    }
+  }
+}
+
+// Slices of each expert's rows for a weight gradient whose tiles fill less
+// than the chip (sized for 256 CUs and rows spread evenly): each slice keeps
+// four steps or more.
+static int wgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
+  const int64_t tiles = E * ((N + gr::BM - 1) / gr::BM) * ((K + gr::BN - 1) / gr::BN);
+  const int64_t steps = (M_total / E + gr::BC - 1) / gr::BC;
+  int64_t s = 256 / tiles;
+  s = s > steps / 4 ? steps / 4 : s;
+  return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
 
 }  // namespace nvfp4
@@ -203,15 +487,20 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   p.N = N;
   p.K = K;
   p.E = (int)E;
-  tile_prefix(expert_offsets, (int)E, M_total, 64, static_cast<int32_t*>(ws), s);
-  const int64_t m_tiles = (M_total + 63) / 64 + E;
-  k_grad_simple<true><<<dim3((unsigned)((K + 63) / 64), (unsigned)m_tiles), 256, 0, s>>>(p);
+  tile_prefix(expert_offsets, (int)E, M_total, gr::BM, static_cast<int32_t*>(ws), s);
+  const int64_t n_tiles = (K + gr::BN - 1) / gr::BN;
+  const int64_t m_tiles = (M_total + gr::BM - 1) / gr::BM + E;   // the most there can be
+  const int64_t blocks = ((m_tiles + 3) / 4 * 4 * n_tiles + 7) / 8 * 8;
+  NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
+             "grouped_w4a16_dgrad: more than 2^22 tiles");
+  k_grad<gr::kDgrad, true><<<(unsigned)blocks, 512, 0, s>>>(p, (int)n_tiles, (int)m_tiles);
   return check_launch("grouped_w4a16_dgrad");
 }
 
 size_t grouped_wgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  (void)E; (void)M_total; (void)N; (void)K;
-  return 256;
+  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 256;
+  const int sp = wgrad_split(E, M_total, N, K);
+  return sp > 1 ? round_up((size_t)sp * (size_t)E * (size_t)N * (size_t)K * 4, 256) : 256;
 }
 
 int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const void* x,
@@ -257,10 +546,37 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   p.N = N;
   p.K = K;
   p.E = (int)E;
-  p.dw_bf16 = dw_bf16;
   p.accumulate = accumulate != 0;
-  k_grad_simple<false><<<dim3((unsigned)((K + 63) / 64), (unsigned)((N + 63) / 64), (unsigned)E),
-                         256, 0, s>>>(p);
+  p.nsplit = wgrad_split(E, M_total, N, K);
+  const int64_t n_tiles = (K + gr::BN - 1) / gr::BN, m_tiles = (N + gr::BM - 1) / gr::BM;
+  // 32 tiles in a row keep an XCD's workgroups on one expert; fewer where the
+  // tiles would not reach every XCD a few times over
+  while (p.run < 5 && (512LL << p.run) <= E * n_tiles * m_tiles) ++p.run;
+  const int64_t round = 8LL << p.run;
+  const int64_t blocks = (E * n_tiles * m_tiles + round - 1) / round * round;
+  NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: more than 2^22 tiles");
+  const bool split = p.nsplit > 1;
+  if (split) {
+    p.dw = ws;
+    p.accumulate = 0;
+  }
+  const dim3 grid((unsigned)blocks, (unsigned)p.nsplit);
+  const int nt = (int)n_tiles, mt = (int)m_tiles;
+  const bool bf = dw_bf16 && !split;
+  if (x_scales && bf) k_grad<gr::kWgradMx, true><<<grid, 512, 0, s>>>(p, nt, mt);
+  else if (x_scales) k_grad<gr::kWgradMx, false><<<grid, 512, 0, s>>>(p, nt, mt);
+  else if (bf) k_grad<gr::kWgrad, true><<<grid, 512, 0, s>>>(p, nt, mt);
+  else k_grad<gr::kWgrad, false><<<grid, 512, 0, s>>>(p, nt, mt);
+  if (split) {
+    const int64_t n = E * N * K;
+    const int64_t g = (n + 1023) / 1024;
+    const unsigned rg = (unsigned)(g < 65536 ? g : 65536);
+    if (dw_bf16)
+      k_wgrad_reduce<true><<<rg, 256, 0, s>>>(static_cast<float*>(ws), n, p.nsplit, dw, 0);
+    else
+      k_wgrad_reduce<false><<<rg, 256, 0, s>>>(static_cast<float*>(ws), n, p.nsplit, dw,
+                                               accumulate != 0);
+  }
   return check_launch("grouped_wgrad");
 }
 
