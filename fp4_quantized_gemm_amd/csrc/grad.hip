@@ -169,7 +169,7 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
   const int tr_c = r32 ^ swz(r16);
   uint32_t off_a[4];             // dgrad: byte offsets of the four loads at step 0
   uint32_t col_a = 0, col_b = 0; // wgrad: byte offset of the lane's chunk in a row
-  int32_t row_a[4], row_b[4];    // wgrad: rows of the next loads (-1: none)
+  uint32_t row_a[4], row_b[4];   // wgrad: the row lists' entries for the next loads
   uint32_t chunk_n[4];           // dgrad: first column of the chunk
   if constexpr (MODE == kDgrad) {
     if (tid < BM) {
@@ -190,18 +190,32 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
     col_a = n < p.N ? (uint32_t)n * 2 : kPastBuffer;
     col_b = k < p.K ? (uint32_t)k * (MODE == kWgrad ? 2 : 1) : kPastBuffer;
   }
+  // A missing list is a buffer of no bytes: the load returns 0 and is not
+  // used.  No branch surrounds these loads: a value merged after a branch
+  // would be waited for there, and every fill in flight with it.
+  const __amdgpu_buffer_rsrc_t rs_ra =
+      buffer_of(p.dy_rows, MODE != kDgrad && p.dy_rows ? (uint64_t)p.M_total * 4 : 0);
+  const __amdgpu_buffer_rsrc_t rs_rb =
+      buffer_of(p.x_rows, MODE != kDgrad && p.x_rows ? (uint64_t)p.M_total * 4 : 0);
+  const uint32_t p_lane = (uint32_t)lo + r16, p_hi = (uint32_t)hi;
   auto load_rows = [&](int step) __attribute__((always_inline)) {
     if constexpr (MODE != kDgrad) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t pr = lo + (int64_t)step * BC + 16 * i + r16;
-        row_a[i] = row_b[i] = -1;
-        if (pr < hi) {
-          row_a[i] = (int32_t)source_row(p.dy_rows, pr, p.M_dy);
-          row_b[i] = (int32_t)source_row(p.x_rows, pr, p.M_x);
-        }
+        const uint32_t o = (p_lane + (uint32_t)step * BC + 16 * i) * 4;
+        row_a[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_ra, o, 0, 0);
+        row_b[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_rb, o, 0, 0);
       }
     }
+  };
+  // byte offset of the lane's chunk in row `listed` (or pr without a list),
+  // past the buffer for rows and columns that are not there
+  auto chunk_at = [&](bool has_list, uint32_t listed, uint32_t pr, int64_t M, uint32_t pitch,
+                      uint32_t col) __attribute__((always_inline)) {
+    const uint32_t t = has_list ? listed : pr;
+    const uint32_t last = (uint32_t)(M - 1);
+    const uint32_t row = (int32_t)t < 0 ? 0u : (t > last ? last : t);
+    return pr < p_hi && col != kPastBuffer ? row * pitch + col : kPastBuffer;
   };
   const uint64_t x_bytes = (uint64_t)p.M_x * (uint64_t)p.K * (MODE == kWgrad ? 2 : 1);
   const __amdgpu_buffer_rsrc_t rs_b =
@@ -238,20 +252,19 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
         const uint32_t o = n0 + chunk_n[i] < (uint32_t)p.N ? off_a[i] : kPastBuffer;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, n0 * 2, 0, 0);
       } else {
-        const uint32_t o = row_a[i] < 0 || col_a == kPastBuffer
-                               ? kPastBuffer : (uint32_t)row_a[i] * N2 + col_a;
+        const uint32_t pr = p_lane + (uint32_t)step * BC + 16 * i;
+        const uint32_t o = chunk_at(p.dy_rows != nullptr, row_a[i], pr, p.M_dy, N2, col_a);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, 0, 0, 0);
+        const uint32_t ob = chunk_at(p.x_rows != nullptr, row_b[i], pr, p.M_x,
+                                     (uint32_t)(p.K * (MODE == kWgrad ? 2 : 1)), col_b);
         if constexpr (MODE == kWgrad) {
-          const uint32_t ob = row_b[i] < 0 || col_b == kPastBuffer
-                                  ? kPastBuffer : (uint32_t)row_b[i] * (uint32_t)(p.K * 2) + col_b;
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, lds_ptr(dst + A_BYTES), 16, ob, 0, 0, 0);
         } else {
-          const bool none = row_b[i] < 0 || col_b == kPastBuffer;
-          const uint32_t ob = none ? kPastBuffer : (uint32_t)row_b[i] * (uint32_t)p.K + col_b;
           const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_b, ob, 0, 0);
           creg[i][0] = v[0];
           creg[i][1] = v[1];
-          sreg[i] = __builtin_amdgcn_raw_buffer_load_b8(rs_s, none ? kPastBuffer : ob >> 5, 0, 0);
+          sreg[i] = __builtin_amdgcn_raw_buffer_load_b8(
+              rs_s, ob == kPastBuffer ? kPastBuffer : ob >> 5, 0, 0);
         }
       }
     }
@@ -507,11 +520,11 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
                   const uint8_t* x_scales, const int32_t* x_rows, int64_t M_x,
                   const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
                   void* dw, int dw_bf16, int accumulate, void* ws, size_t ws_bytes, void* stream) {
-  NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 31) && M_dy >= 0 &&
+  NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 30) && M_dy >= 0 &&
                  M_x >= 0 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 && N < (1LL << 31) &&
                  K < (1LL << 31) && (x_scales == nullptr || K % 32 == 0),
              NVFP4_ERR_SHAPE,
-             "grouped_wgrad: need 1 <= E <= 1024, M_total < 2^31, N %% 8 == 0, K %% 8 == 0 "
+             "grouped_wgrad: need 1 <= E <= 1024, M_total < 2^30, N %% 8 == 0, K %% 8 == 0 "
              "(K %% 32 == 0 for 8-bit x) (E=%lld M_total=%lld N=%lld K=%lld)",
              (long long)E, (long long)M_total, (long long)N, (long long)K);
   NV_REQUIRE((dy_rows != nullptr || M_dy >= M_total) && (x_rows != nullptr || M_x >= M_total),
