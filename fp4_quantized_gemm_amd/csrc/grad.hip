@@ -420,6 +420,329 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Weight gradient.  One workgroup per CU takes 256x256 output tiles (item:
+// slice of the rows, expert, row tile, column tile) one after another, and the
+// loads run on across them: contraction steps of 32 rows go through a ring of
+// four LDS stages, filled three steps ahead, and a tile's outputs are stored
+// while the next tile's first stages are in flight.  (A workgroup per tile
+// waited for its first stage, and for its stores, once per tile: a tile of
+// 1024 rows spent a third of its time there, one of 256 rows half.)
+//
+// Waits.  Loads and stores of a wave complete in order, so step s waits until
+// at most the operations issued after stage s's last fill are outstanding
+// (two steps of kOps, plus the stores where a tile ended in between); each
+// step issues the same number, past the last row too, where they return zeros,
+// and the stores of an edge tile are issued with an offset past the buffer.
+// Row lists are read two steps before the fill that uses them, 8-bit codes
+// three steps before their stage and decoded one step before.
+// ---------------------------------------------------------------------------
+namespace wg {
+constexpr int BM = 256, BN = 256, BC = 32;
+constexpr int A_BYTES = BC * BM * 2;
+constexpr int STAGE = A_BYTES + BC * BN * 2;   // 32768
+constexpr int OUT = 4096;                      // output staging of one wave
+}  // namespace wg
+
+// A contraction step's rows [p, hi) and its tile's first output row and column
+struct WgStep {
+  uint32_t p, hi, a0, b0;
+};
+
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  static_assert(N < 64, "vmcnt has six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <bool MX, bool BF16>
+__global__ void __launch_bounds__(512, 1)
+k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
+  using namespace wg;
+  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t st2[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t st3[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t outb[8 * OUT];
+  // per step: two row-list loads, then two fills of A and two of B (or two
+  // code and two scale loads and two fills of A)
+  constexpr int kOps = MX ? 8 : 6;
+  constexpr int kStores = BF16 ? 16 : 32;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int kg = lane >> 5, r32 = lane & 31;
+  uint8_t* const stage[4] = {st0, st1, st2, st3};
+
+  // ---- items -------------------------------------------------------------
+  const int per_e = n_tiles * m_tiles;
+  const int total = per_e * p.E;
+  const int items = total * p.nsplit;
+  const int xcd = (int)blockIdx.x & 7, loc = (int)blockIdx.x >> 3, per_xcd = (int)gridDim.x >> 3;
+  // the workgroup's i-th item: runs of 2^run items go to the XCDs in turn
+  // (workgroup b runs on XCD b % 8, each with its own L2), and an XCD's
+  // workgroups take its items in turn
+  auto item_at = [&](int i) __attribute__((always_inline)) {
+    const int j = loc + i * per_xcd;
+    return ((((j >> p.run) << 3) + xcd) << p.run) + (j & ((1 << p.run) - 1));
+  };
+  struct Item {
+    uint32_t lo, hi, a0, b0;
+    int e, slice, steps;
+  };
+  auto item_of = [&](int v) __attribute__((always_inline)) {
+    Item t;
+    t.slice = v / total;
+    v -= t.slice * total;
+    t.e = v / per_e;
+    v -= t.e * per_e;
+    const int m = v / n_tiles;
+    t.a0 = (uint32_t)m * BM;
+    t.b0 = (uint32_t)(v - m * n_tiles) * BN;
+    // scalar loads: the offsets do not change, and a vector load here would
+    // wait for every fill in flight
+    const __attribute__((address_space(4))) int32_t* off =
+        (const __attribute__((address_space(4))) int32_t*)p.offsets;
+    const int most = (int)p.M_total;
+    int lo = off[t.e], hi = off[t.e + 1];
+    lo = lo < 0 ? 0 : (lo > most ? most : lo);
+    hi = hi < lo ? lo : (hi > most ? most : hi);
+    if (p.nsplit > 1) {   // whole steps per slice
+      const int per = ((hi - lo + BC - 1) / BC + p.nsplit - 1) / p.nsplit * BC;
+      lo = lo + per * t.slice < hi ? lo + per * t.slice : hi;
+      hi = lo + per < hi ? lo + per : hi;
+    }
+    t.lo = (uint32_t)lo;
+    t.hi = (uint32_t)hi;
+    // a tile's steps are rounded up to the ring's four; the added ones load
+    // zeros and compute nothing
+    t.steps = (hi - lo + 4 * BC - 1) / (4 * BC) * 4;
+    return t;
+  };
+
+  // ---- loads -------------------------------------------------------------
+  // the step that the row lists are next read for
+  int ahead_i = -1, ahead_s = 0;
+  Item ahead;
+  ahead.lo = ahead.hi = ahead.a0 = ahead.b0 = 0;
+  ahead.steps = 0;
+  // (tiles begin at multiples of four: only there a new one can follow)
+  auto next_step = [&](bool maybe_new) __attribute__((always_inline)) {
+    ++ahead_s;
+    while (maybe_new && ahead_s >= ahead.steps) {
+      ahead_s = 0;
+      const int v = item_at(++ahead_i);
+      if (v >= items) {   // none left: rows that are not there
+        ahead.lo = ahead.hi = 0;
+        ahead.steps = 1 << 30;
+      } else {
+        ahead = item_of(v);
+      }
+    }
+    return WgStep{ahead.lo + (uint32_t)ahead_s * BC, ahead.hi, ahead.a0, ahead.b0};
+  };
+  const uint32_t pitch_a = (uint32_t)(p.N * 2), pitch_b = (uint32_t)(p.K * (MX ? 1 : 2));
+  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * pitch_a);
+  const __amdgpu_buffer_rsrc_t rs_b = buffer_of(p.x, (uint64_t)p.M_x * pitch_b);
+  const __amdgpu_buffer_rsrc_t rs_s =
+      buffer_of(p.x_scales, MX ? (uint64_t)p.M_x * (uint64_t)p.K / 32 : 0);
+  // a missing list is a buffer of no bytes: the load returns 0, and is not used
+  const __amdgpu_buffer_rsrc_t rs_ra = buffer_of(p.dy_rows, p.dy_rows ? (uint64_t)p.M_total * 4 : 0);
+  const __amdgpu_buffer_rsrc_t rs_rb = buffer_of(p.x_rows, p.x_rows ? (uint64_t)p.M_total * 4 : 0);
+  // lane's contraction row is 16 i + r16 of the step (i of two), its slot in
+  // the [32][256] tile's row lane % 32, which holds chunk tr_c
+  const int r16 = 2 * wave + kg;
+  const uint32_t tr_c8 = 8u * (uint32_t)(r32 ^ swz(r16));
+  WgStep ring[4];                    // descriptors, row-list entries and codes by step % 4
+  uint32_t ids_a[4], ids_b[4];
+  uint32_t codes[4][2][2], scales[4][2];
+
+  auto load_ids = [&](int u, const WgStep& d) __attribute__((always_inline)) {
+    ring[u] = d;
+    const uint32_t o = (d.p + r32) * 4;
+    ids_a[u] = __builtin_amdgcn_raw_buffer_load_b32(rs_ra, o, 0, 0);
+    ids_b[u] = __builtin_amdgcn_raw_buffer_load_b32(rs_rb, o, 0, 0);
+  };
+  // byte offset of the lane's chunk in the row listed (or the step's own),
+  // past the buffer for rows and columns that are not there
+  auto chunk_at = [&](bool has_list, uint32_t ids, int i, const WgStep& d, uint32_t rows,
+                      uint32_t pitch, uint32_t col, uint32_t cols,
+                      uint32_t bytes) __attribute__((always_inline)) {
+    const uint32_t t0 = __builtin_amdgcn_readlane(ids, 16 * i + 2 * wave);
+    const uint32_t t1 = __builtin_amdgcn_readlane(ids, 16 * i + 2 * wave + 1);
+    const uint32_t pr = d.p + 16 * i + r16;
+    const uint32_t t = has_list ? (kg ? t1 : t0) : pr;
+    const uint32_t row = (int32_t)t < 0 ? 0u : (t < rows ? t : rows - 1);
+    return pr < d.hi && col < cols ? row * pitch + col * bytes : kPastBuffer;
+  };
+  auto issue = [&](uint8_t* st, int u) __attribute__((always_inline)) {
+    const WgStep d = ring[u];
+    uint32_t ob[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ob[i] = chunk_at(p.x_rows != nullptr, ids_b[u], i, d, (uint32_t)p.M_x, pitch_b, d.b0 + tr_c8,
+                       (uint32_t)p.K, MX ? 1 : 2);
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_b, ob[i], 0, 0);
+        codes[u][i][0] = v[0];
+        codes[u][i][1] = v[1];
+        scales[u][i] = __builtin_amdgcn_raw_buffer_load_b8(
+            rs_s, ob[i] == kPastBuffer ? kPastBuffer : ob[i] >> 5, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint8_t* dst = st + (i * 8 + wave) * 1024;
+      const uint32_t oa = chunk_at(p.dy_rows != nullptr, ids_a[u], i, d, (uint32_t)p.M_dy, pitch_a,
+                                   d.a0 + tr_c8, (uint32_t)p.N, 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, oa, 0, 0, 0);
+      if constexpr (!MX)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, lds_ptr(dst + A_BYTES), 16, ob[i], 0, 0, 0);
+    }
+  };
+  auto fill = [&](uint8_t* st, int u) __attribute__((always_inline)) {
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<u32x4*>(st + A_BYTES + (i * 8 + wave) * 1024 + lane * 16) =
+            mx_decode8(make_uint2(codes[u][i][0], codes[u][i][1]), mx_scale(scales[u][i]));
+    }
+  };
+
+  // ---- products ----------------------------------------------------------
+  f32x16_t acc[4][2];
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  };
+  // transposing loads: lane i of a 16-lane group g reads row 8 (g / 2) + 4 h
+  // + i / 4 of the 16-row slice, columns 16 (g % 2) + 4 (i % 4) .. + 3 of the
+  // fragment's 32 (4 chunks); fragment f xors bits 2.. of the chunk
+  const int t_row = 8 * kg + ((lane & 15) >> 2);
+  const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const uint32_t t_off0 = t_row * 512 + ((t_chunk ^ swz(t_row)) << 4) + (lane & 1) * 8;
+  const uint32_t t_off1 = (t_row + 4) * 512 + ((t_chunk ^ swz(t_row + 4)) << 4) + (lane & 1) * 8;
+  auto tr_at = [&](const uint8_t* t, int slice, int f) __attribute__((always_inline)) {
+    const uint32_t x = (uint32_t)f << 6;
+    return tr_frag(t + slice * 8192 + (t_off0 ^ x), t + slice * 8192 + (t_off1 ^ x));
+  };
+  // formed transposed (x as the row operand), so that a lane's four
+  // consecutive accumulators are four consecutive columns of its dw row
+  auto compute = [&](const uint8_t* st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      u32x4 B[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) B[j] = tr_at(st + A_BYTES, s, 2 * wn + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x4 A = tr_at(st, s, 4 * wm + i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(B[j], A, acc[i][j]);
+      }
+    }
+  };
+
+  // ---- outputs: through the wave's own LDS part, 128-byte rows ------------
+  uint8_t* const ob = outb + wave * OUT;
+  auto store = [&](const Item& t) __attribute__((always_inline)) {
+    const int64_t nk = p.N * p.K;
+    const __amdgpu_buffer_rsrc_t rs_o =
+        BF16 ? buffer_of(static_cast<uint16_t*>(p.dw) + t.e * nk, (uint64_t)nk * 2)
+             : buffer_of(static_cast<float*>(p.dw) + ((int64_t)t.slice * p.E + t.e) * nk,
+                         (uint64_t)nk * 4);
+    const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N;
+    const int lr = lane >> 3, lc = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t n0 = t.a0 + 128 * wm + 32 * i;
+      // rows n0 + 8 q + lr, 16-byte chunk lc of the 128-byte piece at column k0
+      auto rows_out = [&](uint32_t k0, uint32_t bytes) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 8 * q + lr;
+          u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
+          const uint32_t n = n0 + r, k = k0 + lc * (16 / bytes);
+          const uint32_t o = n < N && k < K ? (n * K + k) * bytes : kPastBuffer;
+          if constexpr (!BF16) {
+            if (p.accumulate) {
+              const auto old = __builtin_amdgcn_raw_buffer_load_b128(rs_o, o, 0, 0);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(old[c]));
+            }
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, o, 0, 0);
+        }
+      };
+      if constexpr (BF16) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& v = acc[i][j];
+            *reinterpret_cast<uint2*>(ob + r32 * 128 + (((4 * j + q) ^ (r32 & 7)) << 4) + kg * 8) =
+                make_uint2(bf16x2_rne(v[4 * q], v[4 * q + 1]), bf16x2_rne(v[4 * q + 2], v[4 * q + 3]));
+          }
+        rows_out(t.b0 + 64 * wn, 2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& v = acc[i][j];
+            *reinterpret_cast<f32x4*>(ob + r32 * 128 + (((2 * q + kg) ^ (r32 & 7)) << 4)) =
+                f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+          }
+          rows_out(t.b0 + 64 * wn + 32 * j, 4);
+        }
+      }
+    }
+  };
+
+  // ---- the stream --------------------------------------------------------
+  load_ids(0, next_step(true));
+  load_ids(1, next_step(false));
+  load_ids(2, next_step(false));
+#pragma unroll
+  for (int u = 0; u < 3; ++u) issue(stage[u], u);
+  load_ids(3, next_step(false));
+  load_ids(0, next_step(true));   // step 4
+  fill(st0, 0);
+  bool stored = false;
+  for (int i = 0;; ++i) {
+    const int v = item_at(i);
+    if (v >= items) break;
+    const Item t = item_of(v);
+    clear();
+    for (int s = 0; s < t.steps; s += 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < 3 && stored) wait_and_barrier<2 * kOps + kStores>();
+        else wait_and_barrier<2 * kOps>();
+        load_ids((j + 1) & 3, next_step(j == 3));
+        issue(stage[(j + 3) & 3], (j + 3) & 3);
+        fill(stage[(j + 1) & 3], (j + 1) & 3);
+        if (t.lo + (uint32_t)(s + j) * BC < t.hi) compute(stage[j]);
+      }
+      stored = false;
+    }
+    store(t);
+    stored = true;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // fills past the end
+}
+
 // dw = sum of the slices' partial products, in slice order; 4 per lane
 template <bool BF16>
 __global__ void __launch_bounds__(256)
@@ -534,6 +857,8 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   NV_REQUIRE((uint64_t)M_dy < (1ULL << 32) / (2 * (uint64_t)N) &&
                  (uint64_t)M_x < (1ULL << 32) / ((x_scales ? 1 : 2) * (uint64_t)K),
              NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: dy or x exceeds 4 GiB");
+  NV_REQUIRE((uint64_t)N * (uint64_t)K < (1ULL << 30), NVFP4_ERR_UNSUPPORTED,
+             "grouped_wgrad: one expert's dw has 2^30 elements or more");
   NV_REQUIRE(dw_bf16 == 0 || dw_bf16 == 1, NVFP4_ERR_UNSUPPORTED,
              "grouped_wgrad: dw_bf16 must be 0 or 1");
   NV_REQUIRE(!(accumulate && dw_bf16), NVFP4_ERR_UNSUPPORTED,
@@ -562,24 +887,25 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   p.accumulate = accumulate != 0;
   p.nsplit = wgrad_split(E, M_total, N, K);
   const int64_t n_tiles = (K + gr::BN - 1) / gr::BN, m_tiles = (N + gr::BM - 1) / gr::BM;
+  const int64_t items = E * n_tiles * m_tiles * p.nsplit;
+  NV_REQUIRE(items < (1LL << 30), NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: more than 2^30 tiles");
   // 32 tiles in a row keep an XCD's workgroups on one expert; fewer where the
   // tiles would not reach every XCD a few times over
-  while (p.run < 5 && (512LL << p.run) <= E * n_tiles * m_tiles) ++p.run;
-  const int64_t round = 8LL << p.run;
-  const int64_t blocks = (E * n_tiles * m_tiles + round - 1) / round * round;
-  NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: more than 2^22 tiles");
+  while (p.run < 5 && (512LL << p.run) <= items) ++p.run;
+  const int64_t cus = num_cus() / 8 * 8 > 0 ? num_cus() / 8 * 8 : 8;
+  const int64_t want = (items + 7) / 8 * 8;
+  const unsigned grid = (unsigned)(want < cus ? want : cus);
   const bool split = p.nsplit > 1;
   if (split) {
     p.dw = ws;
     p.accumulate = 0;
   }
-  const dim3 grid((unsigned)blocks, (unsigned)p.nsplit);
   const int nt = (int)n_tiles, mt = (int)m_tiles;
   const bool bf = dw_bf16 && !split;
-  if (x_scales && bf) k_grad<gr::kWgradMx, true><<<grid, 512, 0, s>>>(p, nt, mt);
-  else if (x_scales) k_grad<gr::kWgradMx, false><<<grid, 512, 0, s>>>(p, nt, mt);
-  else if (bf) k_grad<gr::kWgrad, true><<<grid, 512, 0, s>>>(p, nt, mt);
-  else k_grad<gr::kWgrad, false><<<grid, 512, 0, s>>>(p, nt, mt);
+  if (x_scales && bf) k_wgrad<true, true><<<grid, 512, 0, s>>>(p, nt, mt);
+  else if (x_scales) k_wgrad<true, false><<<grid, 512, 0, s>>>(p, nt, mt);
+  else if (bf) k_wgrad<false, true><<<grid, 512, 0, s>>>(p, nt, mt);
+  else k_wgrad<false, false><<<grid, 512, 0, s>>>(p, nt, mt);
   if (split) {
     const int64_t n = E * N * K;
     const int64_t g = (n + 1023) / 1024;

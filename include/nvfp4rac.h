@@ -436,8 +436,8 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
  * timing.  dw [E][N][K]: float32, or bf16 with dw_bf16 = 1 (one rounding); an
  * expert without rows gets zeros.  accumulate = 1 (float32 only): the sum is
  * added to what dw holds.  Requires 1 <= E <= 1024, M_total < 2^30,
- * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), M_dy * N * 2 < 2^32,
- * x below 4 GiB; an operand without a row list has at least M_total rows. */
+ * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), N * K < 2^30,
+ * M_dy * N * 2 < 2^32, x below 4 GiB; an operand without a row list has at least M_total rows. */
 size_t grouped_wgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const void* x,
                   const uint8_t* x_scales, const int32_t* x_rows, int64_t M_x,
