@@ -27,7 +27,7 @@ struct GradArgs {
   void* dw;                    // wgrad: [E][N][K] f32 or bf16
   int64_t M_dy, M_x, M_total, N, K;
   int E;
-  int accumulate;
+  int dw_bf16, accumulate;
   int run;                     // wgrad: log2 of the tiles an XCD takes in a row
   int nsplit;                  // wgrad: slices of the rows (blockIdx.y); dw holds their partials
 };
@@ -429,13 +429,20 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
 // waited for its first stage, and for its stores, once per tile: a tile of
 // 1024 rows spent a third of its time there, one of 256 rows half.)
 //
-// Waits.  Loads and stores of a wave complete in order, so step s waits until
-// at most the operations issued after stage s's last fill are outstanding
-// (two steps of kOps, plus the stores where a tile ended in between); each
-// step issues the same number, past the last row too, where they return zeros,
-// and the stores of an edge tile are issued with an offset past the buffer.
-// Row lists are read two steps before the fill that uses them, 8-bit codes
-// three steps before their stage and decoded one step before.
+// Eight waves of 128x64 outputs.  LDS serves 128 bytes per clock: a step's
+// 96 KB of fragment reads and 32 KB of fills take as many clocks as its matrix
+// instructions (1024), so both have to run all the time: fragments are read
+// half a step (16 rows) ahead of their products, in step with the matrix
+// instructions, and the barrier that hands over a stage lies between a step's
+// halves.
+//
+// Waits.  Loads and stores of a wave complete in order, so the barrier of step
+// s waits until at most the operations issued after stage s + 1's last fill
+// are outstanding (two steps of kOps, plus the stores where a tile ended in
+// between); each step issues the same number, past the last row too, where
+// they return zeros, and an edge tile's stores are issued with an offset past
+// the buffer.  Row lists are read two steps before the fill that uses them,
+// 8-bit codes four steps before their stage and decoded two steps later.
 // ---------------------------------------------------------------------------
 namespace wg {
 constexpr int BM = 256, BN = 256, BC = 32;
@@ -451,25 +458,26 @@ struct WgStep {
 
 template <int N>
 __device__ __forceinline__ void wait_and_barrier() {
-  static_assert(N < 64, "vmcnt has six bits");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N < 63 ? N : 63) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-template <bool MX, bool BF16>
+// MX: x is an 8-bit checkpoint.  LA, LB: dy, x are gathered through a row list
+// (without one a row is its step's own, and no per-row arithmetic is left).
+template <bool MX, bool LA, bool LB>
 __global__ void __launch_bounds__(512, 1)
 k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   using namespace wg;
+  // separate objects, and the ring unrolled by four: each access names its
+  // stage, so a fill in flight is not waited for before reads of another
   __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st2[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t st3[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t outb[8 * OUT];
-  // per step: two row-list loads, then two fills of A and two of B (or two
-  // code and two scale loads and two fills of A)
-  constexpr int kOps = MX ? 8 : 6;
-  constexpr int kStores = BF16 ? 16 : 32;
+  constexpr int kOps = (MX ? 6 : 4) + (LA ? 2 : 0) + (LB ? 2 : 0);
+  constexpr int kStores = 16;   // bf16; float32 has 32, and waits for half of them
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -519,7 +527,7 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     t.lo = (uint32_t)lo;
     t.hi = (uint32_t)hi;
     // a tile's steps are rounded up to the ring's four; the added ones load
-    // zeros and compute nothing
+    // and multiply zeros
     t.steps = (hi - lo + 4 * BC - 1) / (4 * BC) * 4;
     return t;
   };
@@ -546,47 +554,57 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     return WgStep{ahead.lo + (uint32_t)ahead_s * BC, ahead.hi, ahead.a0, ahead.b0};
   };
   const uint32_t pitch_a = (uint32_t)(p.N * 2), pitch_b = (uint32_t)(p.K * (MX ? 1 : 2));
-  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * pitch_a);
-  const __amdgpu_buffer_rsrc_t rs_b = buffer_of(p.x, (uint64_t)p.M_x * pitch_b);
-  const __amdgpu_buffer_rsrc_t rs_s =
-      buffer_of(p.x_scales, MX ? (uint64_t)p.M_x * (uint64_t)p.K / 32 : 0);
-  // a missing list is a buffer of no bytes: the load returns 0, and is not used
-  const __amdgpu_buffer_rsrc_t rs_ra = buffer_of(p.dy_rows, p.dy_rows ? (uint64_t)p.M_total * 4 : 0);
-  const __amdgpu_buffer_rsrc_t rs_rb = buffer_of(p.x_rows, p.x_rows ? (uint64_t)p.M_total * 4 : 0);
-  // lane's contraction row is 16 i + r16 of the step (i of two), its slot in
-  // the [32][256] tile's row lane % 32, which holds chunk tr_c
-  const int r16 = 2 * wave + kg;
-  const uint32_t tr_c8 = 8u * (uint32_t)(r32 ^ swz(r16));
+  // of the two 1-KB pieces (two rows) of a [32][256] tile that a wave fills,
+  // piece i is rows 16 i + r16; the lane's slot in the row is lane % 32, which
+  // holds chunk r32 ^ swz(row), columns col8 .. + 7
+  const uint32_t r16 = 2 * wave + kg;
+  const uint32_t col8 = 8u * (uint32_t)(r32 ^ swz(r16));
+  constexpr uint32_t kBytesB = MX ? 1 : 2;
+  const uint32_t at_a = r16 * pitch_a + col8 * 2, at_b = r16 * pitch_b + col8 * kBytesB;
   WgStep ring[4];                    // descriptors, row-list entries and codes by step % 4
-  uint32_t ids_a[4], ids_b[4];
+  uint32_t ids_a[4][2], ids_b[4][2];
   uint32_t codes[4][2][2], scales[4][2];
 
   auto load_ids = [&](int u, const WgStep& d) __attribute__((always_inline)) {
     ring[u] = d;
-    const uint32_t o = (d.p + r32) * 4;
-    ids_a[u] = __builtin_amdgcn_raw_buffer_load_b32(rs_ra, o, 0, 0);
-    ids_b[u] = __builtin_amdgcn_raw_buffer_load_b32(rs_rb, o, 0, 0);
+    const uint64_t n = (uint64_t)p.M_total * 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t o = r16 * 4 + (d.p + 16 * i) * 4;
+      if constexpr (LA)
+        ids_a[u][i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.dy_rows, n), o, 0, 0);
+      if constexpr (LB)
+        ids_b[u][i] = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(p.x_rows, n), o, 0, 0);
+    }
   };
-  // byte offset of the lane's chunk in the row listed (or the step's own),
-  // past the buffer for rows and columns that are not there
-  auto chunk_at = [&](bool has_list, uint32_t ids, int i, const WgStep& d, uint32_t rows,
-                      uint32_t pitch, uint32_t col, uint32_t cols,
-                      uint32_t bytes) __attribute__((always_inline)) {
-    const uint32_t t0 = __builtin_amdgcn_readlane(ids, 16 * i + 2 * wave);
-    const uint32_t t1 = __builtin_amdgcn_readlane(ids, 16 * i + 2 * wave + 1);
-    const uint32_t pr = d.p + 16 * i + r16;
-    const uint32_t t = has_list ? (kg ? t1 : t0) : pr;
-    const uint32_t row = (int32_t)t < 0 ? 0u : (t < rows ? t : rows - 1);
-    return pr < d.hi && col < cols ? row * pitch + col * bytes : kPastBuffer;
+  // Byte offset of the lane's chunk of row 16 i + r16, past the buffer for
+  // rows and columns that are not there.
+  auto chunk_at = [&](auto listed_c, uint32_t id, int i, const WgStep& d, uint32_t c0,
+                      uint32_t cols, uint32_t rows, uint32_t pitch, uint32_t bytes,
+                      uint32_t at) __attribute__((always_inline)) {
+    const bool there = (r16 + 16 * i < d.hi - d.p) & (d.p < d.hi) & (col8 < cols - c0);
+    uint32_t o;
+    if constexpr (decltype(listed_c)::value)
+      o = (id < rows ? id : rows - 1) * pitch + (col8 + c0) * bytes;
+    else
+      o = at + ((d.p + 16 * i) * pitch + c0 * bytes);
+    return there ? o : kPastBuffer;
   };
   auto issue = [&](uint8_t* st, int u) __attribute__((always_inline)) {
     const WgStep d = ring[u];
-    uint32_t ob[2];
+    const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * pitch_a);
+    const __amdgpu_buffer_rsrc_t rs_b = buffer_of(p.x, (uint64_t)p.M_x * pitch_b);
+    uint32_t oa[2], ob[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      ob[i] = chunk_at(p.x_rows != nullptr, ids_b[u], i, d, (uint32_t)p.M_x, pitch_b, d.b0 + tr_c8,
-                       (uint32_t)p.K, MX ? 1 : 2);
+    for (int i = 0; i < 2; ++i) {
+      oa[i] = chunk_at(std::integral_constant<bool, LA>{}, ids_a[u][i], i, d, d.a0, (uint32_t)p.N,
+                       (uint32_t)p.M_dy, pitch_a, 2, at_a);
+      ob[i] = chunk_at(std::integral_constant<bool, LB>{}, ids_b[u][i], i, d, d.b0, (uint32_t)p.K,
+                       (uint32_t)p.M_x, pitch_b, kBytesB, at_b);
+    }
     if constexpr (MX) {
+      const __amdgpu_buffer_rsrc_t rs_s =
+          buffer_of(p.x_scales, (uint64_t)p.M_x * (uint64_t)p.K / 32);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_b, ob[i], 0, 0);
@@ -599,9 +617,7 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint8_t* dst = st + (i * 8 + wave) * 1024;
-      const uint32_t oa = chunk_at(p.dy_rows != nullptr, ids_a[u], i, d, (uint32_t)p.M_dy, pitch_a,
-                                   d.a0 + tr_c8, (uint32_t)p.N, 2);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, oa, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, oa[i], 0, 0, 0);
       if constexpr (!MX)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, lds_ptr(dst + A_BYTES), 16, ob[i], 0, 0, 0);
     }
@@ -632,24 +648,31 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
   const uint32_t t_off0 = t_row * 512 + ((t_chunk ^ swz(t_row)) << 4) + (lane & 1) * 8;
   const uint32_t t_off1 = (t_row + 4) * 512 + ((t_chunk ^ swz(t_row + 4)) << 4) + (lane & 1) * 8;
-  auto tr_at = [&](const uint8_t* t, int slice, int f) __attribute__((always_inline)) {
+  auto tr_at = [&](const uint8_t* t, int f) __attribute__((always_inline)) {
     const uint32_t x = (uint32_t)f << 6;
-    return tr_frag(t + slice * 8192 + (t_off0 ^ x), t + slice * 8192 + (t_off1 ^ x));
+    return tr_frag(t + (t_off0 ^ x), t + (t_off1 ^ x));
+  };
+  u32x4 fa[2][4], fb[2][2];   // by half of the step
+  auto read = [&](const uint8_t* st, int half) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[half][j] = tr_at(st + A_BYTES + half * 8192, 2 * wn + j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fa[half][i] = tr_at(st + half * 8192, 4 * wm + i);
   };
   // formed transposed (x as the row operand), so that a lane's four
   // consecutive accumulators are four consecutive columns of its dw row
-  auto compute = [&](const uint8_t* st) __attribute__((always_inline)) {
+  auto multiply = [&](int half) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      u32x4 B[2];
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) B[j] = tr_at(st + A_BYTES, s, 2 * wn + j);
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[half][j], fa[half][i], acc[i][j]);
+    // a matrix instruction, then up to two LDS reads, five others, one load
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const u32x4 A = tr_at(st, s, 4 * wm + i);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(B[j], A, acc[i][j]);
-      }
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x006, 5, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
   };
 
@@ -657,45 +680,51 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   uint8_t* const ob = outb + wave * OUT;
   auto store = [&](const Item& t) __attribute__((always_inline)) {
     const int64_t nk = p.N * p.K;
-    const __amdgpu_buffer_rsrc_t rs_o =
-        BF16 ? buffer_of(static_cast<uint16_t*>(p.dw) + t.e * nk, (uint64_t)nk * 2)
-             : buffer_of(static_cast<float*>(p.dw) + ((int64_t)t.slice * p.E + t.e) * nk,
-                         (uint64_t)nk * 4);
     const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N;
     const int lr = lane >> 3, lc = lane & 7;
+    // rows n0 + 8 q + lr, 16-byte chunk lc of the 128-byte piece at column k0
+    auto rows_out = [&](const __amdgpu_buffer_rsrc_t& rs_o, uint32_t n0, uint32_t k0,
+                        uint32_t bytes) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t n0 = t.a0 + 128 * wm + 32 * i;
-      // rows n0 + 8 q + lr, 16-byte chunk lc of the 128-byte piece at column k0
-      auto rows_out = [&](uint32_t k0, uint32_t bytes) __attribute__((always_inline)) {
+      for (int q = 0; q < 4; ++q) {
+        const int r = 8 * q + lr;
+        u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
+        const uint32_t n = n0 + r, k = k0 + lc * (16 / bytes);
+        const uint32_t o = n < N && k < K ? (n * K + k) * bytes : kPastBuffer;
+        if (bytes == 4 && p.accumulate) {
+          const auto old = __builtin_amdgcn_raw_buffer_load_b128(rs_o, o, 0, 0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 8 * q + lr;
-          u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
-          const uint32_t n = n0 + r, k = k0 + lc * (16 / bytes);
-          const uint32_t o = n < N && k < K ? (n * K + k) * bytes : kPastBuffer;
-          if constexpr (!BF16) {
-            if (p.accumulate) {
-              const auto old = __builtin_amdgcn_raw_buffer_load_b128(rs_o, o, 0, 0);
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(old[c]));
-            }
-          }
-          __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, o, 0, 0);
+          for (int c = 0; c < 4; ++c)
+            v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(old[c]));
         }
-      };
-      if constexpr (BF16) {
+        // nontemporal: dw is not read back soon, and its lines leave L2 to the
+        // operands (wgrad of 32768 rows, 128 experts of 1536x2048: 0.52 ->
+        // 0.36 ms)
+        __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, o, 0, 2);
+      }
+    };
+    if (p.dw_bf16) {
+      const __amdgpu_buffer_rsrc_t rs_o =
+          buffer_of(static_cast<uint16_t*>(p.dw) + t.e * nk, (uint64_t)nk * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const f32x16_t& v = acc[i][j];
             *reinterpret_cast<uint2*>(ob + r32 * 128 + (((4 * j + q) ^ (r32 & 7)) << 4) + kg * 8) =
-                make_uint2(bf16x2_rne(v[4 * q], v[4 * q + 1]), bf16x2_rne(v[4 * q + 2], v[4 * q + 3]));
+                make_uint2(bf16x2_rne(v[4 * q], v[4 * q + 1]),
+                           bf16x2_rne(v[4 * q + 2], v[4 * q + 3]));
           }
-        rows_out(t.b0 + 64 * wn, 2);
-      } else {
+        rows_out(rs_o, t.a0 + 128 * wm + 32 * i, t.b0 + 64 * wn, 2);
+      }
+    } else {
+      const __amdgpu_buffer_rsrc_t rs_o =
+          buffer_of(static_cast<float*>(p.dw) + ((int64_t)t.slice * p.E + t.e) * nk,
+                    (uint64_t)nk * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -704,9 +733,8 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
             *reinterpret_cast<f32x4*>(ob + r32 * 128 + (((2 * q + kg) ^ (r32 & 7)) << 4)) =
                 f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
           }
-          rows_out(t.b0 + 64 * wn + 32 * j, 4);
+          rows_out(rs_o, t.a0 + 128 * wm + 32 * i, t.b0 + 64 * wn + 32 * j, 4);
         }
-      }
     }
   };
 
@@ -714,29 +742,38 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   load_ids(0, next_step(true));
   load_ids(1, next_step(false));
   load_ids(2, next_step(false));
-#pragma unroll
-  for (int u = 0; u < 3; ++u) issue(stage[u], u);
   load_ids(3, next_step(false));
-  load_ids(0, next_step(true));   // step 4
-  fill(st0, 0);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    issue(stage[u], u);
+    if (u < 2) fill(stage[u], u);
+    if (u == 1) load_ids(0, next_step(true));    // step 4
+    if (u == 2) load_ids(1, next_step(false));   // step 5
+  }
+  wait_and_barrier<2 * kOps>();
+  read(st0, 0);
   bool stored = false;
+  auto body = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      read(stage[j], 1);
+      multiply(0);
+      if (j < 3 && stored) wait_and_barrier<2 * kOps + kStores>();
+      else wait_and_barrier<2 * kOps>();
+      read(stage[(j + 1) & 3], 0);
+      issue(stage[j], j);
+      load_ids((j + 2) & 3, next_step(j == 2));
+      fill(stage[(j + 2) & 3], (j + 2) & 3);
+      multiply(1);
+    }
+    stored = false;
+  };
   for (int i = 0;; ++i) {
     const int v = item_at(i);
     if (v >= items) break;
     const Item t = item_of(v);
     clear();
-    for (int s = 0; s < t.steps; s += 4) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j < 3 && stored) wait_and_barrier<2 * kOps + kStores>();
-        else wait_and_barrier<2 * kOps>();
-        load_ids((j + 1) & 3, next_step(j == 3));
-        issue(stage[(j + 3) & 3], (j + 3) & 3);
-        fill(stage[(j + 1) & 3], (j + 1) & 3);
-        if (t.lo + (uint32_t)(s + j) * BC < t.hi) compute(stage[j]);
-      }
-      stored = false;
-    }
+    for (int s = 0; s < t.steps; s += 4) body();
     store(t);
     stored = true;
   }
@@ -901,11 +938,12 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
     p.accumulate = 0;
   }
   const int nt = (int)n_tiles, mt = (int)m_tiles;
-  const bool bf = dw_bf16 && !split;
-  if (x_scales && bf) k_wgrad<true, true><<<grid, 512, 0, s>>>(p, nt, mt);
-  else if (x_scales) k_wgrad<true, false><<<grid, 512, 0, s>>>(p, nt, mt);
-  else if (bf) k_wgrad<false, true><<<grid, 512, 0, s>>>(p, nt, mt);
-  else k_wgrad<false, false><<<grid, 512, 0, s>>>(p, nt, mt);
+  p.dw_bf16 = dw_bf16 && !split;
+  const auto k = x_scales ? (dy_rows ? (x_rows ? k_wgrad<true, true, true> : k_wgrad<true, true, false>)
+                                     : (x_rows ? k_wgrad<true, false, true> : k_wgrad<true, false, false>))
+                          : (dy_rows ? (x_rows ? k_wgrad<false, true, true> : k_wgrad<false, true, false>)
+                                     : (x_rows ? k_wgrad<false, false, true> : k_wgrad<false, false, false>));
+  k<<<grid, 512, 0, s>>>(p, nt, mt);
   if (split) {
     const int64_t n = E * N * K;
     const int64_t g = (n + 1023) / 1024;
