@@ -45,31 +45,37 @@ __device__ __forceinline__ int64_t source_row(const int32_t* rows, int64_t p, in
 }
 
 // ---------------------------------------------------------------------------
-// 256x256 outputs per workgroup, eight waves (two rows of four, 128x64 each:
-// four by two 32x32 accumulators), contraction 64 at a time through two LDS
-// stages.  "Rows" are dx rows (kDgrad) or dw rows n; columns are k.
+// Both gradients: 256x256 outputs per workgroup, eight waves (two rows of
+// four) of 128x64 outputs each, bf16 32x32x16 matrix instructions.
 //
-// An operand whose contraction index is its slow one (both of wgrad's, the
-// weights of dgrad) lies in LDS as it does in memory, [64][256] bf16, and is
-// read through the transposing LDS load: a group of 16 lanes reads 4
-// contraction rows of 16 columns and each lane gets its column's four values.
-// 16-byte chunk c of contraction row r sits at c ^ swz(r): the four rows of a
-// transposing load then lie in the four 64-byte parts of the 256-byte bank
-// line, and 16 rows of one chunk (the order in which decoded weights are
-// written) in 16 different 16-byte slots, so neither conflicts.
-// dgrad's dy has the contraction fast: [256][64], 16-byte fragment reads,
-// chunk c of row r at c ^ ((r >> 1) & 7).
-// bf16 operands go from memory to LDS directly; 4-bit weights and 8-bit
-// activations are decoded (exactly) on the way, once per workgroup.
+// An operand whose contraction index is its slow one (both of the weight
+// gradient's, the weights of the input gradient) lies in LDS as it does in
+// memory, [contraction][256] bf16, and is read through the transposing LDS
+// load: a group of 16 lanes reads 4 contraction rows of 16 columns and each
+// lane gets its column's four values.  16-byte chunk c of contraction row r
+// sits at c ^ swz(r): the four rows of a transposing load then lie in the four
+// 64-byte parts of the 256-byte bank line, and 16 rows of one chunk (the order
+// in which decoded weights are written) in 16 different 16-byte slots, so
+// neither conflicts.  bf16 operands go from memory to LDS directly; 4-bit
+// weights and 8-bit activations are decoded (exactly) on the way, once per
+// workgroup.
+//
+// LDS serves 128 bytes per clock: for 16 contraction rows the waves read 48 KB
+// and 16 KB are filled, as many clocks as the matrix instructions take (512),
+// so both have to run all the time: fragments are read one slice of 16 ahead
+// of their products, in step with the matrix instructions, and the barrier
+// that hands over a stage lies one slice before the stage's end.  Products are
+// formed transposed (the column operand as matrix rows), so that a lane's four
+// consecutive accumulators are four consecutive columns of its output row.
+//
+// Loads of a wave complete in order, and every step issues the same number of
+// them (past the end too, where they return zeros), so a barrier waits until
+// at most the loads issued after the wanted stage's are outstanding.
 // ---------------------------------------------------------------------------
-namespace gr {
-constexpr int BM = 256, BN = 256, BC = 64;
-constexpr int A_BYTES = BM * BC * 2;
-constexpr int STAGE = A_BYTES + BN * BC * 2;   // 65536
-enum Mode { kDgrad, kWgrad, kWgradMx };
-}  // namespace gr
+constexpr int kTile = 256;
 
-// an offset past every buffer: such a load returns zeros
+// an offset past every buffer: such a load returns zeros, such a store is
+// dropped
 constexpr uint32_t kPastBuffer = 0xFFFFFFF0u;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -84,214 +90,147 @@ __device__ __forceinline__ u32x4 tr_frag(const uint8_t* lo, const uint8_t* hi) {
   return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// Fragments of a [contraction][256] tile: lane i of a 16-lane group g reads
+// row 8 (g / 2) + 4 h + i / 4 of a 16-row slice, columns 16 (g % 2) + 4 (i %
+// 4) .. + 3 of the fragment's 32 (4 chunks); fragment f xors bits 2.. of the
+// chunk.
+struct TrLane {
+  uint32_t off0, off1;
+  __device__ __forceinline__ explicit TrLane(int lane) {
+    const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    off0 = row * 512 + ((chunk ^ swz(row)) << 4) + (lane & 1) * 8;
+    off1 = (row + 4) * 512 + ((chunk ^ swz(row + 4)) << 4) + (lane & 1) * 8;
+  }
+  __device__ __forceinline__ u32x4 at(const uint8_t* slice, int f) const {
+    const uint32_t x = (uint32_t)f << 6;
+    return tr_frag(slice + (off0 ^ x), slice + (off1 ^ x));
+  }
+};
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
                                            kBufferRsrcWord3);
 }
 
-// MODE: which product.  BF16: the output is bf16, staged through LDS for
-// 16-byte row stores (the product is formed transposed, so that a lane holds
-// four consecutive columns); else float32, stored from the accumulators (32
-// lanes write 128 consecutive bytes).
-template <int MODE, bool BF16>
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N < 63 ? N : 63) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Input gradient.  Output rows are the experts' rows, columns k, contraction
+// n, 64 at a time: dy as [256][64] in a ring of three LDS stages, filled three
+// steps ahead (16-byte fragment reads, chunk c of row r at c ^ ((r >> 1) & 7)),
+// the weights as [64][256] in two, decoded one step ahead from registers
+// loaded two steps earlier.
+// ---------------------------------------------------------------------------
+namespace dg {
+constexpr int BC = 64;
+constexpr int A_BYTES = kTile * BC * 2, B_BYTES = BC * kTile * 2;   // 32768 each
+}  // namespace dg
+
 __global__ void __launch_bounds__(512, 1)
-k_grad(GradArgs p, int n_tiles, int m_tiles) {
-  using namespace gr;
-  // two objects, and the loop unrolled by two: each access names its stage,
-  // so the fill of one stage is not waited for before reads of the other
-  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t st1[STAGE];
-  __shared__ int32_t rows_src[MODE == kDgrad ? BM : 1];
+k_dgrad(GradArgs p, int n_tiles) {
+  using namespace dg;
+  // separate objects, and the rings unrolled: each access names its stage, so
+  // a fill in flight is not waited for before reads of another
+  __shared__ __attribute__((aligned(16))) uint8_t sa0[A_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sa1[A_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sa2[A_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sb0[B_BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t sb1[B_BYTES];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int kg = lane >> 5, r32 = lane & 31;
+  uint8_t* const sa[3] = {sa0, sa1, sa2};
+  uint8_t* const sb[2] = {sb0, sb1};
 
-  // tile order (workgroup b runs on XCD b % 8, each with its own L2)
+  // tile: groups of 4 row tiles x all column tiles, a contiguous range of
+  // that order per XCD (workgroup b runs on XCD b % 8, each with its own L2)
   int e, nt;
   int64_t lo, hi, a0;
   {
     const int b = (int)blockIdx.x;
-    if constexpr (MODE == kDgrad) {
-      // groups of 4 row tiles x all column tiles, a contiguous range per XCD
-      const int real_m = p.prefix[p.E];
-      const int real_blocks = ((real_m + 3) / 4) * 4 * n_tiles;
-      const int per_xcd = (real_blocks + 7) / 8;
-      if ((b >> 3) >= per_xcd) return;
-      const int v = (b & 7) * per_xcd + (b >> 3);
-      if (v >= real_blocks) return;
-      const int group = 4 * n_tiles;
-      const int gi = v / group, g = v - gi * group;
-      const int gm = real_m - 4 * gi < 4 ? real_m - 4 * gi : 4;
-      const int gt = 4 * gi + g % gm;
-      nt = g / gm;
-      if (gt >= real_m || nt >= n_tiles) return;
-      int l = 0, h = p.E;
-      while (h - l > 1) {
-        const int mid = (l + h) >> 1;
-        if (p.prefix[mid] <= gt) l = mid; else h = mid;
-      }
-      e = l;
-      expert_rows(p, e, lo, hi);
-      a0 = lo + (int64_t)(gt - p.prefix[e]) * BM;
-    } else {
-      // runs of 2^run tiles of an expert go to the XCDs in turn
-      const int per_e = n_tiles * m_tiles;
-      const int total = per_e * p.E;
-      const int loc = b >> 3, run = p.run;
-      const int v = ((((loc >> run) << 3) + (b & 7)) << run) + (loc & ((1 << run) - 1));
-      if (v >= total) return;
-      e = v / per_e;
-      const int t = v - e * per_e;
-      nt = t % n_tiles;
-      a0 = (int64_t)(t / n_tiles) * BM;
-      expert_rows(p, e, lo, hi);
-      if (p.nsplit > 1) {   // this slice's rows: whole steps
-        const int64_t steps = (hi - lo + BC - 1) / BC;
-        const int64_t per = (steps + p.nsplit - 1) / p.nsplit * BC;
-        const int64_t l = lo + per * blockIdx.y;
-        lo = l < hi ? l : hi;
-        hi = lo + per < hi ? lo + per : hi;
-      }
-    }
+    const int real_m = p.prefix[p.E];
+    const int real_blocks = ((real_m + 3) / 4) * 4 * n_tiles;
+    const int per_xcd = (real_blocks + 7) / 8;
+    if ((b >> 3) >= per_xcd) return;
+    const int v = (b & 7) * per_xcd + (b >> 3);
+    if (v >= real_blocks) return;
+    const int group = 4 * n_tiles;
+    const int gi = v / group, g = v - gi * group;
+    const int gm = real_m - 4 * gi < 4 ? real_m - 4 * gi : 4;
+    const int gt = 4 * gi + g % gm;
+    nt = g / gm;
+    if (gt >= real_m || nt >= n_tiles) return;
+    // the last expert whose first tile is at or before gt: 64 at a time
+    int n = 0;
+    for (int i = 0; i < p.E; i += 64)
+      n += __builtin_popcountll(__ballot(i + lane < p.E && p.prefix[i + lane] <= gt));
+    e = __builtin_amdgcn_readfirstlane(n - 1);
+    expert_rows(p, e, lo, hi);
+    a0 = lo + (int64_t)(gt - p.prefix[e]) * kTile;
   }
-  const int64_t b0 = (int64_t)nt * BN;
-  const int steps = MODE == kDgrad ? (int)((p.N + BC - 1) / BC) : (int)((hi - lo + BC - 1) / BC);
+  const int64_t b0 = (int64_t)nt * kTile;
+  const int steps = (int)((p.N + BC - 1) / BC);
 
   // ---- loads -------------------------------------------------------------
   const uint32_t N2 = (uint32_t)(p.N * 2);
-  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * (uint64_t)p.N * 2);
-  // [64][256] tiles: lane's contraction row is 16 i + r16 of the step (i of
-  // four), its slot in the row lane % 32, which holds chunk tr_c
-  const int r16 = 2 * wave + kg;
-  const int tr_c = r32 ^ swz(r16);
-  uint32_t off_a[4];             // dgrad: byte offsets of the four loads at step 0
-  uint32_t col_a = 0, col_b = 0; // wgrad: byte offset of the lane's chunk in a row
-  uint32_t row_a[4], row_b[4];   // wgrad: the row lists' entries for the next loads
-  uint32_t chunk_n[4];           // dgrad: first column of the chunk
-  if constexpr (MODE == kDgrad) {
-    if (tid < BM) {
-      int64_t pr = a0 + tid;
-      if (pr >= hi) pr = hi - 1;
-      rows_src[tid] = (int32_t)source_row(p.dy_rows, pr, p.M_dy);
-    }
-    __syncthreads();
+  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * N2);
+  // of the 32 1-KB pieces (8 rows) of a dy stage, piece 8 i + wave; the lane
+  // takes chunk a_c of row 64 i + 8 wave + lane / 8
+  const uint32_t a_c = (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+  uint32_t off_a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = (i * 8 + wave) * 64 + lane;
-      const int r = q >> 3, c = (q & 7) ^ ((r >> 1) & 7);
-      off_a[i] = (uint32_t)rows_src[r] * N2 + 16u * c;
-      chunk_n[i] = 8u * c;
-    }
-  } else {
-    const int64_t n = a0 + 8 * tr_c, k = b0 + 8 * tr_c;
-    col_a = n < p.N ? (uint32_t)n * 2 : kPastBuffer;
-    col_b = k < p.K ? (uint32_t)k * (MODE == kWgrad ? 2 : 1) : kPastBuffer;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t pr = a0 + 64 * i + 8 * wave + (lane >> 3);
+    off_a[i] = pr < hi ? (uint32_t)source_row(p.dy_rows, pr, p.M_dy) * N2 + 16u * a_c : kPastBuffer;
   }
-  // A missing list is a buffer of no bytes: the load returns 0 and is not
-  // used.  No branch surrounds these loads: a value merged after a branch
-  // would be waited for there, and every fill in flight with it.
-  const __amdgpu_buffer_rsrc_t rs_ra =
-      buffer_of(p.dy_rows, MODE != kDgrad && p.dy_rows ? (uint64_t)p.M_total * 4 : 0);
-  const __amdgpu_buffer_rsrc_t rs_rb =
-      buffer_of(p.x_rows, MODE != kDgrad && p.x_rows ? (uint64_t)p.M_total * 4 : 0);
-  const uint32_t p_lane = (uint32_t)lo + r16, p_hi = (uint32_t)hi;
-  auto load_rows = [&](int step) __attribute__((always_inline)) {
-    if constexpr (MODE != kDgrad) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t o = (p_lane + (uint32_t)step * BC + 16 * i) * 4;
-        row_a[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_ra, o, 0, 0);
-        row_b[i] = __builtin_amdgcn_raw_buffer_load_b32(rs_rb, o, 0, 0);
-      }
-    }
-  };
-  // byte offset of the lane's chunk in row `listed` (or pr without a list),
-  // past the buffer for rows and columns that are not there
-  auto chunk_at = [&](bool has_list, uint32_t listed, uint32_t pr, int64_t M, uint32_t pitch,
-                      uint32_t col) __attribute__((always_inline)) {
-    const uint32_t t = has_list ? listed : pr;
-    const uint32_t last = (uint32_t)(M - 1);
-    const uint32_t row = (int32_t)t < 0 ? 0u : (t > last ? last : t);
-    return pr < p_hi && col != kPastBuffer ? row * pitch + col : kPastBuffer;
-  };
-  const uint64_t x_bytes = (uint64_t)p.M_x * (uint64_t)p.K * (MODE == kWgrad ? 2 : 1);
-  const __amdgpu_buffer_rsrc_t rs_b =
-      MODE == kDgrad ? buffer_of(p.w_codes + e * packed_codes_per_expert(p.N, p.K),
-                                 (uint64_t)p.N * p.K / 2)
-                     : buffer_of(p.x, x_bytes);
+  const __amdgpu_buffer_rsrc_t rs_w =
+      buffer_of(p.w_codes + e * packed_codes_per_expert(p.N, p.K), (uint64_t)p.N * p.K / 2);
   const __amdgpu_buffer_rsrc_t rs_s =
-      MODE == kDgrad ? buffer_of(p.w_scales + e * packed_scales_per_expert(p.N, p.K),
-                                 (uint64_t)p.N * p.K / 16)
-                     : buffer_of(p.x_scales, (uint64_t)p.M_x * (uint64_t)p.K / 32);
-  // dgrad weights: wave w takes the step's code tiles 2 w, 2 w + 1 (of 4 row
-  // blocks x 4 column tiles), lane l one row's half tile: 16 bytes = 32 k
+      buffer_of(p.w_scales + e * packed_scales_per_expert(p.N, p.K), (uint64_t)p.N * p.K / 16);
+  // weights: wave w takes the step's code tiles 2 w, 2 w + 1 (of 4 row blocks
+  // x 4 column tiles), a lane one row's half tile: 16 bytes = 32 columns
   const int w_rb = (2 * wave + kg) >> 2, w_ct = (2 * wave + kg) & 3;
   const int w_half = (lane >> 4) & 1, w_row = lane & 15;
-  uint32_t off_w = 0, off_ws = 0;
-  const uint32_t w_step = (uint32_t)(4 * (p.K >> 6) * 512);
-  if constexpr (MODE == kDgrad) {
-    int64_t kt = (b0 >> 6) + w_ct;
-    if (kt >= (p.K >> 6)) kt = (p.K >> 6) - 1;   // columns past K are never stored
-    const uint32_t tile = (uint32_t)(w_rb * (p.K >> 6) + kt);
-    off_w = tile * 512 + w_half * 256 + w_row * 16;
-    off_ws = tile * 64 + w_row * 4 + w_half * 2;
-  }
-  u32x4 wreg;
-  uint32_t sreg[4];
-  uint32_t creg[4][2];
-
-  auto issue = [&](uint8_t* st, int step) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint8_t* dst = st + (i * 8 + wave) * 1024;
-      if constexpr (MODE == kDgrad) {
-        const uint32_t n0 = (uint32_t)step * BC;
-        const uint32_t o = n0 + chunk_n[i] < (uint32_t)p.N ? off_a[i] : kPastBuffer;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, n0 * 2, 0, 0);
-      } else {
-        const uint32_t pr = p_lane + (uint32_t)step * BC + 16 * i;
-        const uint32_t o = chunk_at(p.dy_rows != nullptr, row_a[i], pr, p.M_dy, N2, col_a);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(dst), 16, o, 0, 0, 0);
-        const uint32_t ob = chunk_at(p.x_rows != nullptr, row_b[i], pr, p.M_x,
-                                     (uint32_t)(p.K * (MODE == kWgrad ? 2 : 1)), col_b);
-        if constexpr (MODE == kWgrad) {
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_b, lds_ptr(dst + A_BYTES), 16, ob, 0, 0, 0);
-        } else {
-          const auto v = __builtin_amdgcn_raw_buffer_load_b64(rs_b, ob, 0, 0);
-          creg[i][0] = v[0];
-          creg[i][1] = v[1];
-          sreg[i] = __builtin_amdgcn_raw_buffer_load_b8(
-              rs_s, ob == kPastBuffer ? kPastBuffer : ob >> 5, 0, 0);
-        }
-      }
-    }
-    if constexpr (MODE == kDgrad) {
-      const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs_b, off_w, (uint32_t)step * w_step, 0);
-      wreg = u32x4{v[0], v[1], v[2], v[3]};
-      sreg[0] = __builtin_amdgcn_raw_buffer_load_b16(rs_s, off_ws, (uint32_t)step * (w_step >> 3), 0);
-    }
-    load_rows(step + 1);
+  const uint32_t k_tiles = (uint32_t)(p.K >> 6);
+  const uint32_t kt = (uint32_t)(b0 >> 6) + w_ct;   // columns past K are never stored
+  const uint32_t w_tile = w_rb * k_tiles + (kt < k_tiles ? kt : k_tiles - 1);
+  const uint32_t off_w = w_tile * 512 + w_half * 256 + w_row * 16;
+  const uint32_t off_ws = w_tile * 64 + w_row * 4 + w_half * 2;
+  const uint32_t w_step = 4 * k_tiles * 512;
+  u32x4 wcodes[2];
+  uint32_t wscales[2];
+  // (rows of the weights past N lie past the buffer)
+  auto issue_w = [&](int set, int u) __attribute__((always_inline)) {
+    const bool there = u < steps;
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs_w, there ? off_w : kPastBuffer,
+                                                         there ? (uint32_t)u * w_step : 0, 0);
+    wcodes[set] = u32x4{v[0], v[1], v[2], v[3]};
+    wscales[set] = __builtin_amdgcn_raw_buffer_load_b16(
+        rs_s, there ? off_ws : kPastBuffer, there ? (uint32_t)u * (w_step >> 3) : 0, 0);
   };
-  // decode what issue() left in registers into the stage
-  auto fill = [&](uint8_t* st) __attribute__((always_inline)) {
-    if constexpr (MODE == kDgrad) {
-      const float s0 = e4m3_decode(sreg[0] & 0xFFu), s1 = e4m3_decode(sreg[0] >> 8);
-      const int r = 16 * w_rb + w_row;
+  auto issue_a = [&](uint8_t* st, int u) __attribute__((always_inline)) {
+    const bool there = (uint32_t)u * BC + 8 * a_c < (uint32_t)p.N;
+    const uint32_t so = u < steps ? (uint32_t)u * (2 * BC) : 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 8 * w_ct + 4 * w_half + j;
-        *reinterpret_cast<u32x4*>(st + A_BYTES + r * 512 + ((c ^ swz(w_row)) << 4)) =
-            decode8_bf16(wreg[j], j < 2 ? s0 : s1);
-      }
-    } else if constexpr (MODE == kWgradMx) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x4*>(st + A_BYTES + (i * 8 + wave) * 1024 + lane * 16) =
-            mx_decode8(make_uint2(creg[i][0], creg[i][1]), mx_scale(sreg[i]));
-    }
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(st + (i * 8 + wave) * 1024), 16,
+                                               there ? off_a[i] : kPastBuffer, so, 0, 0);
+  };
+  // chunk j (8 columns) of the lane's 32 into the weight stage
+  const uint32_t f_row = 16 * w_rb + w_row, f_chunk = 8 * w_ct + 4 * w_half;
+  auto fill = [&](uint8_t* st, int set, int j) __attribute__((always_inline)) {
+    const float s = e4m3_decode(j < 2 ? wscales[set] & 0xFFu : wscales[set] >> 8);
+    *reinterpret_cast<u32x4*>(st + f_row * 512 + (((f_chunk + j) ^ swz(w_row)) << 4)) =
+        decode8_bf16(wcodes[set][j], s);
   };
 
   // ---- products ----------------------------------------------------------
@@ -302,121 +241,108 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
-  // transposing loads: lane i of a 16-lane group g reads row 8 (g / 2) + 4 h
-  // + i / 4 of the 16-row slice, columns 16 (g % 2) + 4 (i % 4) .. + 3 of the
-  // fragment's 32 (4 chunks)
-  const int t_row = 8 * kg + ((lane & 15) >> 2);
-  const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  const uint32_t t_off0 = t_row * 512 + ((t_chunk ^ swz(t_row)) << 4) + (lane & 1) * 8;
-  const uint32_t t_off1 = (t_row + 4) * 512 + ((t_chunk ^ swz(t_row + 4)) << 4) + (lane & 1) * 8;
-  // fragment f (32 columns = 4 chunks, 64 bytes): chunk bits 2.. are xored too
-  auto tr_at = [&](const uint8_t* t, int slice, int f) __attribute__((always_inline)) {
-    const uint32_t x = (uint32_t)f << 6;   // f < 8: bits 6..8 of the slot's byte offset
-    return tr_frag(t + slice * 8192 + (t_off0 ^ x), t + slice * 8192 + (t_off1 ^ x));
-  };
-  const int sw = (r32 >> 1) & 7;
-  auto compute = [&](const uint8_t* st, auto nv_c) __attribute__((always_inline)) {
-    constexpr int NV = decltype(nv_c)::value;
+  const TrLane tr(lane);
+  const uint32_t a_row = (wm * 128 + r32) * 128;
+  const int a_sw = (r32 >> 1) & 7;
+  u32x4 fa[2][4], fb[2][2];   // by slice % 2
+  auto read = [&](const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 B[2];
+    for (int j = 0; j < 2; ++j) fb[s & 1][j] = tr.at(b + s * 8192, 2 * wn + j);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) B[j] = tr_at(st + A_BYTES, s, 2 * wn + j);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        u32x4 A;
-        if constexpr (MODE == kDgrad)
-          A = *reinterpret_cast<const u32x4*>(st + (wm * 128 + 32 * i + r32) * 128 +
-                                              (((2 * s + kg) ^ sw) << 4));
-        else
-          A = tr_at(st, s, 4 * wm + i);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = BF16 ? mfma32_bf16(B[j], A, acc[i][j]) : mfma32_bf16(A, B[j], acc[i][j]);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      fa[s & 1][i] = *reinterpret_cast<const u32x4*>(a + a_row + 32 * i * 128 +
+                                                     (((2 * s + kg) ^ a_sw) << 4));
   };
-  auto kstep = [&](const uint8_t* cur, uint8_t* nxt, int s, auto nv_c) __attribute__((always_inline)) {
-    if (s + 1 < steps) issue(nxt, s + 1);
-    compute(cur, nv_c);
-    if (s + 1 < steps) fill(nxt);
-    wait_vmem0();
-    __syncthreads();
-  };
-  auto run = [&](auto nv_c) __attribute__((always_inline)) {
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
-      kstep(st0, st1, s, nv_c);
-      kstep(st1, st0, s + 1, nv_c);
-    }
-    if (s < steps) kstep(st0, st1, s, nv_c);
-  };
-  load_rows(0);
-  if (steps > 0) {
-    issue(st0, 0);
-    fill(st0);
-  }
-  wait_vmem0();
-  __syncthreads();
-  if constexpr (MODE == kDgrad) {
-    // rows of this wave inside the expert: only their 32-row blocks
-    const int64_t vr = hi - a0 - wm * 128;
-    if (vr > 64) run(std::integral_constant<int, 4>{});
-    else if (vr > 32) run(std::integral_constant<int, 2>{});
-    else if (vr > 0) run(std::integral_constant<int, 1>{});
-    else run(std::integral_constant<int, 0>{});
-  } else {
-    run(std::integral_constant<int, 4>{});
-  }
-
-  // ---- outputs -----------------------------------------------------------
-  const float sc = MODE == kDgrad ? p.g_w[e] : 1.0f;
-  if constexpr (BF16) {
-    // row 32 i + r32 of the wave's half tile, columns 64 wn + 32 j + 8 q +
-    // 4 kg .. + 3; 16-byte chunk c of row r at c ^ (r & 15)
-    uint8_t* half = wm ? st1 : st0;
+  auto multiply = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
+    // a matrix instruction, then an LDS read, vector instructions, a load
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 32 * i + r32, c = 8 * wn + 4 * j + q;
-          const f32x16_t& v = acc[i][j];
-          *reinterpret_cast<uint2*>(half + r * 512 + ((c ^ (r & 15)) << 4) + kg * 8) =
-              make_uint2(bf16x2_rne(v[4 * q] * sc, v[4 * q + 1] * sc),
-                         bf16x2_rne(v[4 * q + 2] * sc, v[4 * q + 3] * sc));
-        }
-    __syncthreads();
-    const int64_t rows_end = MODE == kDgrad ? hi : p.N;
-    uint16_t* out = MODE == kDgrad ? p.dx
-                                   : static_cast<uint16_t*>(p.dw) + (int64_t)e * p.N * p.K;
-#pragma unroll 4
-    for (int q = tid; q < BM * 32; q += 512) {
-      const int r = q >> 5, c = q & 31;
-      const int64_t a = a0 + r, k = b0 + 8 * c;
-      const uint8_t* src = (r < 128 ? st0 : st1) + (r & 127) * 512 + ((c ^ (r & 15)) << 4);
-      if (a < rows_end && k < p.K)
-        *reinterpret_cast<uint4*>(out + a * p.K + k) = *reinterpret_cast<const uint4*>(src);
+    for (int i = 0; i < 8; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x006, 5, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
-  } else {
-    float* out = static_cast<float*>(p.dw) +
-                 ((int64_t)(p.nsplit > 1 ? blockIdx.y : 0) * p.E + e) * p.N * p.K;
+  };
+  // step u: dy stage AU, weight stage BU
+  auto step = [&](auto au_c, auto bu_c, int u) __attribute__((always_inline)) {
+    constexpr int AU = decltype(au_c)::value, BU = decltype(bu_c)::value;
+    read(sa[AU], sb[BU], 1);
+    fill(sb[BU ^ 1], BU ^ 1, 0);
+    multiply(0);
+    read(sa[AU], sb[BU], 2);
+    fill(sb[BU ^ 1], BU ^ 1, 1);
+    multiply(1);
+    read(sa[AU], sb[BU], 3);
+    fill(sb[BU ^ 1], BU ^ 1, 2);
+    fill(sb[BU ^ 1], BU ^ 1, 3);
+    multiply(2);
+    wait_and_barrier<6>();
+    issue_w(BU ^ 1, u + 3);
+    issue_a(sa[AU], u + 3);
+    read(sa[(AU + 1) % 3], sb[BU ^ 1], 0);
+    multiply(3);
+  };
+  issue_w(0, 0);
+  issue_a(sa0, 0);
+  issue_w(1, 1);
+  issue_a(sa1, 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int j = 0; j < 4; ++j) fill(sb0, 0, j);
+  issue_w(0, 2);
+  issue_a(sa2, 2);
+  wait_and_barrier<12>();
+  read(sa0, sb0, 0);
+  using c0 = std::integral_constant<int, 0>;
+  using c1 = std::integral_constant<int, 1>;
+  using c2 = std::integral_constant<int, 2>;
+  for (int u = 0;;) {
+    step(c0{}, c0{}, u);
+    if (++u == steps) break;
+    step(c1{}, c1{}, u);
+    if (++u == steps) break;
+    step(c2{}, c0{}, u);
+    if (++u == steps) break;
+    step(c0{}, c1{}, u);
+    if (++u == steps) break;
+    step(c1{}, c0{}, u);
+    if (++u == steps) break;
+    step(c2{}, c1{}, u);
+    if (++u == steps) break;
+  }
+  wait_and_barrier<0>();
+
+  // ---- outputs: through the wave's own LDS part, 128-byte rows ------------
+  const float sc = p.g_w[e];
+  uint8_t* const ob = sa0 + wave * 4096;
+  const uint32_t K = (uint32_t)p.K;
+  // (rows past the expert's last lie past the buffer)
+  const __amdgpu_buffer_rsrc_t rs_o =
+      buffer_of(p.dx + a0 * p.K, (uint64_t)(hi - a0 < kTile ? hi - a0 : kTile) * K * 2);
+  const int lr = lane >> 3, lc = lane & 7;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t k = b0 + 64 * wn + 32 * j + r32;
-        if (k >= p.K) continue;
+  for (int i = 0; i < 4; ++i) {
+    if (hi - a0 - wm * 128 <= 32 * i) break;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t a = a0 + 128 * wm + 32 * i + 8 * (r >> 2) + 4 * kg + (r & 3);
-          if (a >= p.N) continue;
-          float* d = out + a * p.K + k;
-          *d = p.accumulate ? *d + acc[i][j][r] : acc[i][j][r];
-        }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& v = acc[i][j];
+        *reinterpret_cast<uint2*>(ob + r32 * 128 + (((4 * j + q) ^ (r32 & 7)) << 4) + kg * 8) =
+            make_uint2(bf16x2_rne(v[4 * q] * sc, v[4 * q + 1] * sc),
+                       bf16x2_rne(v[4 * q + 2] * sc, v[4 * q + 3] * sc));
       }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t r = 8 * q + lr;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
+      const uint32_t k = (uint32_t)b0 + 64 * wn + 8 * lc;
+      __builtin_amdgcn_raw_buffer_store_b128(
+          v, rs_o, k < K ? ((128 * wm + 32 * i + r) * K + k) * 2 : kPastBuffer, 0, 0);
+    }
   }
 }
 
@@ -429,14 +355,7 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
 // waited for its first stage, and for its stores, once per tile: a tile of
 // 1024 rows spent a third of its time there, one of 256 rows half.)
 //
-// Eight waves of 128x64 outputs.  LDS serves 128 bytes per clock: a step's
-// 96 KB of fragment reads and 32 KB of fills take as many clocks as its matrix
-// instructions (1024), so both have to run all the time: fragments are read
-// half a step (16 rows) ahead of their products, in step with the matrix
-// instructions, and the barrier that hands over a stage lies between a step's
-// halves.
-//
-// Waits.  Loads and stores of a wave complete in order, so the barrier of step
+// Waits: stores complete in order with the loads, so the barrier of step
 // s waits until at most the operations issued after stage s + 1's last fill
 // are outstanding (two steps of kOps, plus the stores where a tile ended in
 // between); each step issues the same number, past the last row too, where
@@ -445,9 +364,9 @@ k_grad(GradArgs p, int n_tiles, int m_tiles) {
 // 8-bit codes four steps before their stage and decoded two steps later.
 // ---------------------------------------------------------------------------
 namespace wg {
-constexpr int BM = 256, BN = 256, BC = 32;
-constexpr int A_BYTES = BC * BM * 2;
-constexpr int STAGE = A_BYTES + BC * BN * 2;   // 32768
+constexpr int BC = 32;
+constexpr int A_BYTES = BC * kTile * 2;
+constexpr int STAGE = 2 * A_BYTES;             // 32768
 constexpr int OUT = 4096;                      // output staging of one wave
 }  // namespace wg
 
@@ -455,13 +374,6 @@ constexpr int OUT = 4096;                      // output staging of one wave
 struct WgStep {
   uint32_t p, hi, a0, b0;
 };
-
-template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N < 63 ? N : 63) : "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // MX: x is an 8-bit checkpoint.  LA, LB: dy, x are gathered through a row list
 // (without one a row is its step's own, and no per-row arithmetic is left).
@@ -509,8 +421,8 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     t.e = v / per_e;
     v -= t.e * per_e;
     const int m = v / n_tiles;
-    t.a0 = (uint32_t)m * BM;
-    t.b0 = (uint32_t)(v - m * n_tiles) * BN;
+    t.a0 = (uint32_t)m * kTile;
+    t.b0 = (uint32_t)(v - m * n_tiles) * kTile;
     // scalar loads: the offsets do not change, and a vector load here would
     // wait for every fill in flight
     const __attribute__((address_space(4))) int32_t* off =
@@ -641,26 +553,14 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   };
-  // transposing loads: lane i of a 16-lane group g reads row 8 (g / 2) + 4 h
-  // + i / 4 of the 16-row slice, columns 16 (g % 2) + 4 (i % 4) .. + 3 of the
-  // fragment's 32 (4 chunks); fragment f xors bits 2.. of the chunk
-  const int t_row = 8 * kg + ((lane & 15) >> 2);
-  const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  const uint32_t t_off0 = t_row * 512 + ((t_chunk ^ swz(t_row)) << 4) + (lane & 1) * 8;
-  const uint32_t t_off1 = (t_row + 4) * 512 + ((t_chunk ^ swz(t_row + 4)) << 4) + (lane & 1) * 8;
-  auto tr_at = [&](const uint8_t* t, int f) __attribute__((always_inline)) {
-    const uint32_t x = (uint32_t)f << 6;
-    return tr_frag(t + (t_off0 ^ x), t + (t_off1 ^ x));
-  };
+  const TrLane tr(lane);
   u32x4 fa[2][4], fb[2][2];   // by half of the step
   auto read = [&](const uint8_t* st, int half) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) fb[half][j] = tr_at(st + A_BYTES + half * 8192, 2 * wn + j);
+    for (int j = 0; j < 2; ++j) fb[half][j] = tr.at(st + A_BYTES + half * 8192, 2 * wn + j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) fa[half][i] = tr_at(st + half * 8192, 4 * wm + i);
+    for (int i = 0; i < 4; ++i) fa[half][i] = tr.at(st + half * 8192, 4 * wm + i);
   };
-  // formed transposed (x as the row operand), so that a lane's four
-  // consecutive accumulators are four consecutive columns of its dw row
   auto multiply = [&](int half) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -802,8 +702,8 @@ k_wgrad_reduce(const float* __restrict__ part, int64_t n, int nsplit, void* __re
 // than the chip (sized for 256 CUs and rows spread evenly): each slice keeps
 // four steps or more.
 static int wgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  const int64_t tiles = E * ((N + gr::BM - 1) / gr::BM) * ((K + gr::BN - 1) / gr::BN);
-  const int64_t steps = (M_total / E + gr::BC - 1) / gr::BC;
+  const int64_t tiles = E * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile);
+  const int64_t steps = (M_total / E + 63) / 64;
   int64_t s = 256 / tiles;
   s = s > steps / 4 ? steps / 4 : s;
   return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
@@ -860,13 +760,13 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   p.N = N;
   p.K = K;
   p.E = (int)E;
-  tile_prefix(expert_offsets, (int)E, M_total, gr::BM, static_cast<int32_t*>(ws), s);
-  const int64_t n_tiles = (K + gr::BN - 1) / gr::BN;
-  const int64_t m_tiles = (M_total + gr::BM - 1) / gr::BM + E;   // the most there can be
+  tile_prefix(expert_offsets, (int)E, M_total, kTile, static_cast<int32_t*>(ws), s);
+  const int64_t n_tiles = (K + kTile - 1) / kTile;
+  const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
   const int64_t blocks = ((m_tiles + 3) / 4 * 4 * n_tiles + 7) / 8 * 8;
   NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
              "grouped_w4a16_dgrad: more than 2^22 tiles");
-  k_grad<gr::kDgrad, true><<<(unsigned)blocks, 512, 0, s>>>(p, (int)n_tiles, (int)m_tiles);
+  k_dgrad<<<(unsigned)blocks, 512, 0, s>>>(p, (int)n_tiles);
   return check_launch("grouped_w4a16_dgrad");
 }
 
@@ -923,7 +823,7 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   p.E = (int)E;
   p.accumulate = accumulate != 0;
   p.nsplit = wgrad_split(E, M_total, N, K);
-  const int64_t n_tiles = (K + gr::BN - 1) / gr::BN, m_tiles = (N + gr::BM - 1) / gr::BM;
+  const int64_t n_tiles = (K + kTile - 1) / kTile, m_tiles = (N + kTile - 1) / kTile;
   const int64_t items = E * n_tiles * m_tiles * p.nsplit;
   NV_REQUIRE(items < (1LL << 30), NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: more than 2^30 tiles");
   // 32 tiles in a row keep an XCD's workgroups on one expert; fewer where the
