@@ -29,7 +29,8 @@ struct GradArgs {
   int E;
   int dw_bf16, accumulate;
   int run;                     // wgrad: log2 of the tiles an XCD takes in a row
-  int nsplit;                  // wgrad: slices of the rows (blockIdx.y); dw holds their partials
+  int nsplit;                  // slices of the contraction
+  float* part;                 // dgrad: their float32 parts [nsplit][M_total][K]
 };
 
 __device__ __forceinline__ void expert_rows(const GradArgs& p, int e, int64_t& lo, int64_t& hi) {
@@ -120,12 +121,57 @@ __device__ __forceinline__ void wait_and_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Input gradient, one 32x64 block of a wave: sc * acc to columns k0 .. + 63 of
+// rows r0 .. r0 + 31 of a matrix of `rows` rows of K at `out` (bf16, or the
+// float32 part of a slice), through 4 KB of the wave's own LDS in 128-byte
+// rows.
+template <typename T>
+__device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2], float sc, T* out,
+                                          int64_t rows, uint32_t r0, uint32_t k0, uint32_t K) {
+  constexpr bool kF32 = sizeof(T) == 4;
+  const int lane = threadIdx.x & 63;
+  const int kg = lane >> 5, r32 = lane & 31, lr = lane >> 3, lc = lane & 7;
+  // (rows past the last lie past the buffer)
+  const __amdgpu_buffer_rsrc_t rs = buffer_of(out, (uint64_t)rows * K * sizeof(T));
+#pragma unroll
+  for (int h = 0; h < (kF32 ? 2 : 1); ++h) {
+    if constexpr (kF32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& v = acc[h];
+        *reinterpret_cast<f32x4*>(own + r32 * 128 + (((2 * q + kg) ^ (r32 & 7)) << 4)) =
+            f32x4{v[4 * q] * sc, v[4 * q + 1] * sc, v[4 * q + 2] * sc, v[4 * q + 3] * sc};
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& v = acc[j];
+          *reinterpret_cast<uint2*>(own + r32 * 128 + (((4 * j + q) ^ (r32 & 7)) << 4) + kg * 8) =
+              make_uint2(bf16x2_rne(v[4 * q] * sc, v[4 * q + 1] * sc),
+                         bf16x2_rne(v[4 * q + 2] * sc, v[4 * q + 3] * sc));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t r = 8 * q + lr;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 128 + ((lc ^ (r & 7)) << 4));
+      const uint32_t k = k0 + 32 * h + lc * (16 / sizeof(T));
+      __builtin_amdgcn_raw_buffer_store_b128(
+          v, rs, k < K ? ((r0 + r) * K + k) * (uint32_t)sizeof(T) : kPastBuffer, 0, 0);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Input gradient.  Output rows are the experts' rows, columns k, contraction
 // n, 64 at a time: dy as [256][64] in a ring of three LDS stages, filled three
 // steps ahead (16-byte fragment reads, chunk c of row r at c ^ ((r >> 1) & 7)),
 // the weights as [64][256] in two, decoded one step ahead from registers
-// loaded two steps earlier.
+// loaded two steps earlier.  Where the tiles fill less than the chip the
+// contraction is split: each slice writes its float32 part (times g_w), and
+// k_dgrad_join adds them in slice order.
 // ---------------------------------------------------------------------------
 namespace dg {
 constexpr int BC = 64;
@@ -178,7 +224,10 @@ k_dgrad(GradArgs p, int n_tiles) {
     a0 = lo + (int64_t)(gt - p.prefix[e]) * kTile;
   }
   const int64_t b0 = (int64_t)nt * kTile;
-  const int steps = (int)((p.N + BC - 1) / BC);
+  // this slice's steps (all of them without a split)
+  const int all = (int)((p.N + BC - 1) / BC);
+  const int per = (all + p.nsplit - 1) / p.nsplit;
+  const int u0 = (int)blockIdx.y * per, u1 = u0 + per < all ? u0 + per : all;
 
   // ---- loads -------------------------------------------------------------
   const uint32_t N2 = (uint32_t)(p.N * 2);
@@ -210,7 +259,7 @@ k_dgrad(GradArgs p, int n_tiles) {
   uint32_t wscales[2];
   // (rows of the weights past N lie past the buffer)
   auto issue_w = [&](int set, int u) __attribute__((always_inline)) {
-    const bool there = u < steps;
+    const bool there = u < u1;
     const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs_w, there ? off_w : kPastBuffer,
                                                          there ? (uint32_t)u * w_step : 0, 0);
     wcodes[set] = u32x4{v[0], v[1], v[2], v[3]};
@@ -218,8 +267,8 @@ k_dgrad(GradArgs p, int n_tiles) {
         rs_s, there ? off_ws : kPastBuffer, there ? (uint32_t)u * (w_step >> 3) : 0, 0);
   };
   auto issue_a = [&](uint8_t* st, int u) __attribute__((always_inline)) {
-    const bool there = (uint32_t)u * BC + 8 * a_c < (uint32_t)p.N;
-    const uint32_t so = u < steps ? (uint32_t)u * (2 * BC) : 0;
+    const bool there = u < u1 && (uint32_t)u * BC + 8 * a_c < (uint32_t)p.N;
+    const uint32_t so = u < u1 ? (uint32_t)u * (2 * BC) : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(st + (i * 8 + wave) * 1024), 16,
@@ -234,36 +283,49 @@ k_dgrad(GradArgs p, int n_tiles) {
   };
 
   // ---- products ----------------------------------------------------------
-  f32x16_t acc[4][2];
+  const TrLane tr(lane);
+  const int a_sw = (r32 >> 1) & 7;
+  issue_w(0, u0);
+  issue_a(sa0, u0);
+  issue_w(1, u0 + 1);
+  issue_a(sa1, u0 + 1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int j = 0; j < 4; ++j) fill(sb0, 0, j);
+  issue_w(0, u0 + 2);
+  issue_a(sa2, u0 + 2);
+  wait_and_barrier<12>();
+  // the tile with NV 32-row blocks per row of waves; whole, so that no
+  // accumulator is merged between variants
+  auto whole = [&](auto nv_c) __attribute__((always_inline)) {
+  constexpr int NV = decltype(nv_c)::value;
+  f32x16_t acc[NV][2];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const TrLane tr(lane);
-  const uint32_t a_row = (wm * 128 + r32) * 128;
-  const int a_sw = (r32 >> 1) & 7;
-  u32x4 fa[2][4], fb[2][2];   // by slice % 2
+  const uint32_t a_row = (wm * 32 * NV + r32) * 128;
+  u32x4 fa[2][NV], fb[2][2];   // by slice % 2
   auto read = [&](const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) fb[s & 1][j] = tr.at(b + s * 8192, 2 * wn + j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NV; ++i)
       fa[s & 1][i] = *reinterpret_cast<const u32x4*>(a + a_row + 32 * i * 128 +
                                                      (((2 * s + kg) ^ a_sw) << 4));
   };
   auto multiply = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
-    // a matrix instruction, then an LDS read, vector instructions, a load
+    // a matrix instruction, then LDS reads, vector instructions, a load
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2 * NV; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x006, 5, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, NV == 4 ? 1 : NV == 2 ? 2 : 3, 0);
+      __builtin_amdgcn_sched_group_barrier(0x006, NV == 4 ? 5 : 10, 0);
       __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
   };
@@ -286,63 +348,197 @@ k_dgrad(GradArgs p, int n_tiles) {
     read(sa[(AU + 1) % 3], sb[BU ^ 1], 0);
     multiply(3);
   };
-  issue_w(0, 0);
-  issue_a(sa0, 0);
-  issue_w(1, 1);
-  issue_a(sa1, 1);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) fill(sb0, 0, j);
-  issue_w(0, 2);
-  issue_a(sa2, 2);
-  wait_and_barrier<12>();
   read(sa0, sb0, 0);
   using c0 = std::integral_constant<int, 0>;
   using c1 = std::integral_constant<int, 1>;
   using c2 = std::integral_constant<int, 2>;
-  for (int u = 0;;) {
+  for (int u = u0; u < u1;) {
     step(c0{}, c0{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
     step(c1{}, c1{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
     step(c2{}, c0{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
     step(c0{}, c1{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
     step(c1{}, c0{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
     step(c2{}, c1{}, u);
-    if (++u == steps) break;
+    if (++u >= u1) break;
   }
   wait_and_barrier<0>();
 
-  // ---- outputs: through the wave's own LDS part, 128-byte rows ------------
   const float sc = p.g_w[e];
-  uint8_t* const ob = sa0 + wave * 4096;
-  const uint32_t K = (uint32_t)p.K;
-  // (rows past the expert's last lie past the buffer)
-  const __amdgpu_buffer_rsrc_t rs_o =
-      buffer_of(p.dx + a0 * p.K, (uint64_t)(hi - a0 < kTile ? hi - a0 : kTile) * K * 2);
-  const int lr = lane >> 3, lc = lane & 7;
+  const int64_t rows = hi - a0 < kTile ? hi - a0 : kTile;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (hi - a0 - wm * 128 <= 32 * i) break;
+  for (int i = 0; i < NV; ++i) {
+    const uint32_t r0 = 32 * (NV * wm + i), k0 = (uint32_t)b0 + 64 * wn;
+    if (p.nsplit == 1)
+      dgrad_out(sa0 + wave * 4096, acc[i], sc, p.dx + a0 * p.K, rows, r0, k0, (uint32_t)p.K);
+    else
+      dgrad_out(sa0 + wave * 4096, acc[i], sc,
+                p.part + ((int64_t)blockIdx.y * p.M_total + a0) * p.K, rows, r0, k0,
+                (uint32_t)p.K);
+  }
+  };
+  if (hi - a0 > 128) whole(std::integral_constant<int, 4>{});
+  else if (hi - a0 > 64) whole(std::integral_constant<int, 2>{});
+  else whole(std::integral_constant<int, 1>{});
+}
+
+// ---------------------------------------------------------------------------
+// Input gradient for few rows per expert: the weights' bytes bound it, so each
+// wave streams a strip of 64 columns over its range of n by itself, without a
+// barrier: the codes of 64 rows x 64 columns go from memory to registers two
+// steps ahead, are decoded into the wave's own 8 KB of LDS and read back
+// through the transposing load; dy's fragments come from memory (the four
+// waves of a workgroup, four strips of one expert, share them in L1).  32 rows
+// of the expert per pass; more re-stream the weights.
+// ---------------------------------------------------------------------------
+namespace dgf {
+constexpr int BC = 64;
+}  // namespace dgf
+
+__global__ void __launch_bounds__(256, 3)
+k_dgrad_few(GradArgs p, int groups) {
+  using namespace dgf;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * 8192];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = lane >> 5, r32 = lane & 31;
+  uint8_t* const own = lds + wave * 8192;
+
+  int b = (int)blockIdx.x;
+  const int slice = b % p.nsplit;
+  b /= p.nsplit;
+  const int e = b / groups;
+  const uint32_t k0 = (uint32_t)((b - e * groups) * 4 + wave) * 64;
+  const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N;
+  if (k0 >= K) return;
+  int64_t lo, hi;
+  expert_rows(p, e, lo, hi);
+  if (lo >= hi) return;
+  // this slice's steps
+  const int all = (int)((p.N + BC - 1) / BC);
+  const int per = (all + p.nsplit - 1) / p.nsplit;
+  const int u0 = slice * per < all ? slice * per : all;
+  const int u1 = u0 + per < all ? u0 + per : all;
+
+  const uint32_t N2 = N * 2;
+  const __amdgpu_buffer_rsrc_t rs_a = buffer_of(p.dy, (uint64_t)p.M_dy * N2);
+  const __amdgpu_buffer_rsrc_t rs_w =
+      buffer_of(p.w_codes + e * packed_codes_per_expert(p.N, p.K), (uint64_t)p.N * p.K / 2);
+  const __amdgpu_buffer_rsrc_t rs_s =
+      buffer_of(p.w_scales + e * packed_scales_per_expert(p.N, p.K), (uint64_t)p.N * p.K / 16);
+  // load i of two: row block 2 i + kg of the step's four, one row's half tile
+  const int w_half = (lane >> 4) & 1, w_row = lane & 15;
+  const uint32_t k_tiles = K >> 6;
+  const uint32_t w_step = 4 * k_tiles * 512;
+  uint32_t off_w[2], off_ws[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t tile = (2 * i + kg) * k_tiles + (k0 >> 6);
+    off_w[i] = tile * 512 + w_half * 256 + w_row * 16;
+    off_ws[i] = tile * 64 + w_row * 4 + w_half * 2;
+  }
+  u32x4 wcodes[2][2];
+  uint32_t wscales[2][2];
+  // nontemporal: each code byte is read once (a line of scales serves two
+  // strips)
+  auto load_w = [&](int set, int u) __attribute__((always_inline)) {
+    const uint32_t so = u < u1 ? (uint32_t)u * w_step : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const auto v =
+          __builtin_amdgcn_raw_buffer_load_b128(rs_w, u < u1 ? off_w[i] : kPastBuffer, so, 2);
+      wcodes[set][i] = u32x4{v[0], v[1], v[2], v[3]};
+      wscales[set][i] = __builtin_amdgcn_raw_buffer_load_b16(
+          rs_s, u < u1 ? off_ws[i] : kPastBuffer, so >> 3, 0);
+    }
+  };
+  // the wave's [64][64] tile: 128-byte rows, chunk c of row r at c ^ wz(r):
+  // four rows of a transposing load in four 64-byte bank parts, 16 rows of one
+  // chunk (a write) in 16 slots
+  auto wz = [](int r) __attribute__((always_inline)) { return ((r & 2) << 1) | ((r >> 2) & 3); };
+  auto fill = [&](int set) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float s0 = e4m3_decode(wscales[set][i] & 0xFFu), s1 = e4m3_decode(wscales[set][i] >> 8);
+      const int r = 16 * (2 * i + kg) + w_row;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<u32x4*>(own + r * 128 + (((4 * w_half + j) ^ wz(w_row)) << 4)) =
+            decode8_bf16(wcodes[set][i][j], j < 2 ? s0 : s1);
+    }
+  };
+  const int t_row = 8 * kg + ((lane & 15) >> 2);
+  const int t_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  const uint32_t t_off0 = t_row * 128 + ((t_chunk ^ wz(t_row)) << 4) + (lane & 1) * 8;
+  const uint32_t t_off1 = (t_row + 4) * 128 + ((t_chunk ^ wz(t_row + 4)) << 4) + (lane & 1) * 8;
+  const float sc = p.g_w[e];
+
+  for (int64_t r0 = lo; r0 < hi; r0 += 32) {
+    const int64_t pr = r0 + r32;
+    const uint32_t off_a =
+        pr < hi ? (uint32_t)source_row(p.dy_rows, pr, p.M_dy) * N2 + 16u * kg : kPastBuffer;
+    f32x16_t acc[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x16_t& v = acc[i][j];
-        *reinterpret_cast<uint2*>(ob + r32 * 128 + (((4 * j + q) ^ (r32 & 7)) << 4) + kg * 8) =
-            make_uint2(bf16x2_rne(v[4 * q] * sc, v[4 * q + 1] * sc),
-                       bf16x2_rne(v[4 * q + 2] * sc, v[4 * q + 3] * sc));
-      }
+      for (int r = 0; r < 16; ++r) acc[j][r] = 0.f;
+    u32x4 fa[2][4];
+    auto load_a = [&](int set, int u) __attribute__((always_inline)) {
+      const uint32_t so = u < u1 ? (uint32_t)u * (2 * BC) : 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t r = 8 * q + lr;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
-      const uint32_t k = (uint32_t)b0 + 64 * wn + 8 * lc;
-      __builtin_amdgcn_raw_buffer_store_b128(
-          v, rs_o, k < K ? ((128 * wm + 32 * i + r) * K + k) * 2 : kPastBuffer, 0, 0);
+      for (int s = 0; s < 4; ++s) {
+        const bool there = u < u1 && (uint32_t)u * BC + 16 * s < N && off_a != kPastBuffer;
+        const auto v =
+            __builtin_amdgcn_raw_buffer_load_b128(rs_a, there ? off_a + 32 * s : kPastBuffer, so, 0);
+        fa[set][s] = u32x4{v[0], v[1], v[2], v[3]};
+      }
+    };
+    auto step = [&](auto set_c, int u) __attribute__((always_inline)) {
+      constexpr int SET = decltype(set_c)::value;
+      fill(SET);
+      load_a(SET ^ 1, u + 1);
+      load_w(SET, u + 2);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[j] = mfma32_bf16(tr_frag(own + s * 2048 + (t_off0 ^ (j << 6)),
+                                       own + s * 2048 + (t_off1 ^ (j << 6))),
+                               fa[SET][s], acc[j]);
+    };
+    load_a(0, u0);
+    load_w(0, u0);
+    load_w(1, u0 + 1);
+    for (int u = u0; u < u1; u += 2) {
+      step(std::integral_constant<int, 0>{}, u);
+      if (u + 1 < u1) step(std::integral_constant<int, 1>{}, u + 1);
     }
+    const int64_t rows = hi - r0 < 32 ? hi - r0 : 32;
+    if (p.nsplit == 1)
+      dgrad_out(own, acc, sc, p.dx + r0 * p.K, rows, 0, k0, K);
+    else
+      dgrad_out(own, acc, sc, p.part + ((int64_t)slice * p.M_total + r0) * p.K, rows, 0, k0, K);
+  }
+}
+
+// dx = sum of the slices' parts, in slice order, over the experts' rows; four
+// columns per lane
+__global__ void __launch_bounds__(256)
+k_dgrad_join(const float* __restrict__ part, const int32_t* __restrict__ offsets, int E,
+             int64_t M_total, int64_t K, int nsplit, uint16_t* __restrict__ dx) {
+  int64_t lo = offsets[0], hi = offsets[E];
+  lo = lo < 0 ? 0 : lo;
+  hi = hi > M_total ? M_total : hi;
+  const int64_t n = M_total * K;
+  for (int64_t q = lo * K + (blockIdx.x * 256LL + threadIdx.x) * 4; q < hi * K;
+       q += gridDim.x * 1024LL) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(part + q);
+    for (int i = 1; i < nsplit; ++i) s += *reinterpret_cast<const f32x4*>(part + i * n + q);
+    *reinterpret_cast<uint2*>(dx + q) = make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
   }
 }
 
@@ -680,6 +876,27 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // fills past the end
 }
 
+// The input gradient's few-row kernel: up to 32 rows per expert on average.
+static bool dgrad_few_rows(int64_t E, int64_t M_total) { return M_total <= 32 * E; }
+
+// Slices of n, at most 16, each of eight steps of 64 or more: for the few-row
+// kernel, enough for four waves per SIMD of 256 CUs if every expert (at most
+// one per row) has rows; for the tiled one, enough to give every CU a tile
+// where the rows make less than one per two CUs.
+static int dgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
+  const int64_t steps = (N + 63) / 64;
+  int64_t s;
+  if (dgrad_few_rows(E, M_total)) {
+    s = 4096 / ((E < M_total ? E : (M_total < 1 ? 1 : M_total)) * (K / 64));
+  } else {
+    s = 256 / ((M_total + kTile - 1) / kTile * ((K + kTile - 1) / kTile));
+  }
+  s = s > steps / 8 ? steps / 8 : s;
+  s = s < 1 ? 1 : (s > 16 ? 16 : s);
+  const int64_t per = (steps + s - 1) / s;
+  return (int)((steps + per - 1) / per);   // no slice is empty
+}
+
 // dw = sum of the slices' partial products, in slice order; 4 per lane
 template <bool BF16>
 __global__ void __launch_bounds__(256)
@@ -715,9 +932,13 @@ using namespace nvfp4;
 
 extern "C" {
 
+static size_t dgrad_prefix_bytes(int64_t E) { return round_up((size_t)(E + 1) * sizeof(int32_t), 256); }
+
 size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  (void)M_total; (void)N; (void)K;
-  return round_up((size_t)((E < 1 ? 1 : E) + 1) * sizeof(int32_t), 256);
+  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 256;
+  const int sp = dgrad_split(E, M_total, N, K);
+  return dgrad_prefix_bytes(E) +
+         (sp > 1 ? round_up((size_t)sp * (size_t)M_total * (size_t)K * 4, 256) : 0);
 }
 
 int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
@@ -760,13 +981,28 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   p.N = N;
   p.K = K;
   p.E = (int)E;
-  tile_prefix(expert_offsets, (int)E, M_total, kTile, static_cast<int32_t*>(ws), s);
-  const int64_t n_tiles = (K + kTile - 1) / kTile;
-  const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
-  const int64_t blocks = ((m_tiles + 3) / 4 * 4 * n_tiles + 7) / 8 * 8;
-  NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
-             "grouped_w4a16_dgrad: more than 2^22 tiles");
-  k_dgrad<<<(unsigned)blocks, 512, 0, s>>>(p, (int)n_tiles);
+  p.nsplit = dgrad_split(E, M_total, N, K);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + dgrad_prefix_bytes(E));
+  if (dgrad_few_rows(E, M_total)) {
+    const int64_t groups = (K + 255) / 256;
+    const int64_t blocks = E * groups * p.nsplit;
+    NV_REQUIRE(blocks < (1LL << 23), NVFP4_ERR_UNSUPPORTED,
+               "grouped_w4a16_dgrad: more than 2^23 tiles");
+    k_dgrad_few<<<(unsigned)blocks, 256, 0, s>>>(p, (int)groups);
+  } else {
+    const int64_t n_tiles = (K + kTile - 1) / kTile;
+    const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
+    const int64_t blocks = ((m_tiles + 3) / 4 * 4 * n_tiles + 7) / 8 * 8;
+    NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
+               "grouped_w4a16_dgrad: more than 2^22 tiles");
+    tile_prefix(expert_offsets, (int)E, M_total, kTile, static_cast<int32_t*>(ws), s);
+    k_dgrad<<<dim3((unsigned)blocks, (unsigned)p.nsplit), 512, 0, s>>>(p, (int)n_tiles);
+  }
+  if (p.nsplit > 1) {
+    const int64_t g = (M_total * K + 1023) / 1024;
+    k_dgrad_join<<<(unsigned)(g < 65536 ? g : 65536), 256, 0, s>>>(
+        p.part, expert_offsets, (int)E, M_total, K, p.nsplit, p.dx);
+  }
   return check_launch("grouped_w4a16_dgrad");
 }
 
