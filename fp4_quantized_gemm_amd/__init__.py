@@ -203,26 +203,27 @@ def _need(t, dtype, name):
 
 def _arg(t, dtype, name, dev, shape=None, optional=False, strided=False):
     """Check one tensor argument: on dev, of the dtype, of the shape (None
-    entries are free), contiguous (strided: rows may be padded)."""
-    if t is None:
-        if optional:
-            return
-        raise NvfpError(f"{name} is required")
+    entries are free), contiguous (strided: rows may be padded).  Returns its
+    address (None for an optional tensor that is not there)."""
+    if t is None and optional:
+        return None
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise NvfpError(f"{name} must be a device tensor")
     if t.device != dev:
         raise NvfpError(f"{name} is on {t.device}, the call is on {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise NvfpError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or
-                              any(w is not None and w != n for w, n in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape and \
+            (t.dim() != len(shape) or
+             any(w is not None and w != n for w, n in zip(shape, t.shape))):
         raise NvfpError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if strided:
+    if not t.is_contiguous():
+        if not strided:
+            raise NvfpError(f"{name} must be contiguous")
         if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
                 (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
             raise NvfpError(f"{name} must have contiguous rows")
-    elif not t.is_contiguous():
-        raise NvfpError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _ld(t):
@@ -232,12 +233,14 @@ def _ld(t):
 
 def _call(name, dev, *args):
     """One library call on dev's current stream, with dev the current device."""
-    fn = getattr(_load(), name)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)), name)
+    fn = getattr(_lib or _load(), name)
+    if dev.index == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), name)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != 0:
+        _check(st, name)
 
 
 class QdqWeights(NamedTuple):
@@ -580,16 +583,18 @@ def mxfp8_checkpoint(x, glu=False, want_codes=True):
     [M][K] u8 E4M3, scales [M][K/32] u8 E8M0, h).  glu=True: x = [gate | up]
     and h [M][K/2] bf16 = silu(gate) * up from the same read; h is None
     otherwise.  want_codes=False (with glu): h alone."""
-    _arg(x, torch.bfloat16, "x", getattr(x, "device", None), (None, None), strided=True)
+    dev = getattr(x, "device", None)
+    xp = _arg(x, torch.bfloat16, "x", dev, (None, None), strided=True)
     M, K = x.shape
-    dev = x.device
-    codes = scales = h = None
+    codes = scales = h = cp = sp = hp = None
     if want_codes:
         codes = torch.empty((M, K), dtype=torch.uint8, device=dev)
         scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+        cp, sp = codes.data_ptr(), scales.data_ptr()
     if glu:
         h = torch.empty((M, K // 2), dtype=torch.bfloat16, device=dev)
-    _call("mxfp8_checkpoint", dev, _ptr(x), M, K, _ld(x), _ptr(codes), _ptr(scales), _ptr(h))
+        hp = h.data_ptr()
+    _call("mxfp8_checkpoint", dev, xp, M, K, _ld(x), cp, sp, hp)
     return dict(codes=codes, scales=scales, h=h)
 
 
@@ -597,24 +602,28 @@ def mxfp8_restore(codes, scales, out=None):
     """The bf16 values [M][K] that a checkpoint's codes and scales stand for
     (exact).  out: a bf16 tensor to write, whose rows may be strided."""
     dev = getattr(codes, "device", None)
-    _arg(codes, torch.uint8, "codes", dev, (None, None))
+    cp = _arg(codes, torch.uint8, "codes", dev, (None, None))
     M, K = codes.shape
-    _arg(scales, torch.uint8, "scales", dev, (M, K // 32))
-    _arg(out, torch.bfloat16, "out", dev, (M, K), optional=True, strided=True)
-    x = out if out is not None else torch.empty((M, K), dtype=torch.bfloat16, device=dev)
-    _call("mxfp8_restore", dev, _ptr(codes), _ptr(scales), M, K, _ptr(x), _ld(x))
-    return x
+    sp = _arg(scales, torch.uint8, "scales", dev, (M, K // 32))
+    xp = _arg(out, torch.bfloat16, "out", dev, (M, K), optional=True, strided=True)
+    if out is None:
+        out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        xp = out.data_ptr()
+    _call("mxfp8_restore", dev, cp, sp, M, K, xp, _ld(out))
+    return out
 
 
-def _m_total(M_total, *row_lists):
-    """Rows of the permuted side: as given, else a row list's length."""
+def _m_total(M_total, default, *row_lists):
+    """Rows of the permuted side: as given, else a row list's length, else
+    the default."""
     for rows in row_lists:
-        if M_total is None and rows is not None:
-            M_total = int(rows.numel())
-    for rows in row_lists:
-        if rows is not None and rows.numel() < M_total:
-            raise NvfpError("a row list is shorter than M_total")
-    return M_total
+        if rows is not None:
+            n = rows.shape[0]
+            if M_total is None:
+                M_total = n
+            elif n < M_total:
+                raise NvfpError("a row list is shorter than M_total")
+    return default if M_total is None else M_total
 
 
 def grouped_w4a16_dgrad(dy, dy_rows, w_codes, w_scales, g_w, expert_offsets, M_total=None,
@@ -625,25 +634,25 @@ def grouped_w4a16_dgrad(dy, dy_rows, w_codes, w_scales, g_w, expert_offsets, M_t
     as they were."""
     dev = getattr(dy, "device", None)
     _arg(dy, torch.bfloat16, "dy", dev, (None, None))
-    M_src = dy.shape[0]
     E, N = _wshape(w_codes)
-    K = int(w_codes.shape[3]) * 64
-    _arg(dy, torch.bfloat16, "dy", dev, (None, N))
-    _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
-    _arg(w_codes, torch.uint8, "w_codes", dev)
-    _arg(w_scales, torch.uint8, "w_scales", dev, (E, 2, N // 16, K // 64, 16, 4))
-    _arg(g_w, torch.float32, "g_w", dev, (E,))
-    _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
-    M_total = _m_total(M_total, dy_rows)
-    if M_total is None:
-        M_total = M_src
-    _arg(out, torch.bfloat16, "out", dev, (M_total, K), optional=True)
-    dx = out if out is not None else torch.empty((M_total, K), dtype=torch.bfloat16, device=dev)
-    ws = _ws(_load().grouped_w4a16_dgrad_workspace_size(E, M_total, N, K), dev)
-    _call("grouped_w4a16_dgrad", dev, _ptr(dy), _ptr(dy_rows), M_src, _ptr(w_codes),
-          _ptr(w_scales), _ptr(g_w), _ptr(expert_offsets), E, M_total, N, K, _ptr(dx), _ptr(ws),
-          ws.numel())
-    return dx
+    K = w_codes.shape[3] * 64
+    dyp = _arg(dy, torch.bfloat16, "dy", dev, (None, N))
+    M_src = dy.shape[0]
+    rp = _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
+    wp = _arg(w_codes, torch.uint8, "w_codes", dev)
+    wsp = _arg(w_scales, torch.uint8, "w_scales", dev, (E, 2, N // 16, K // 64, 16, 4))
+    gp = _arg(g_w, torch.float32, "g_w", dev, (E,))
+    op = _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
+    M_total = _m_total(M_total, M_src, dy_rows)
+    xp = _arg(out, torch.bfloat16, "out", dev, (M_total, K), optional=True)
+    if out is None:
+        out = torch.empty((M_total, K), dtype=torch.bfloat16, device=dev)
+        xp = out.data_ptr()
+    nb = (_lib or _load()).grouped_w4a16_dgrad_workspace_size(E, M_total, N, K)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _call("grouped_w4a16_dgrad", dev, dyp, rp, M_src, wp, wsp, gp, op, E, M_total, N, K, xp,
+          ws.data_ptr(), nb)
+    return out
 
 
 def grouped_wgrad(dy, dy_rows, x, x_rows, expert_offsets, x_scales=None, M_total=None,
@@ -653,30 +662,30 @@ def grouped_wgrad(dy, dy_rows, x, x_rows, expert_offsets, x_scales=None, M_total
     x_scales, gathered by x_rows).  dtype float32 or bfloat16; out: a tensor
     to write, with accumulate=True (float32) to add to."""
     dev = getattr(dy, "device", None)
-    _arg(dy, torch.bfloat16, "dy", dev, (None, None))
-    _arg(x, torch.bfloat16 if x_scales is None else torch.uint8, "x", dev, (None, None))
+    dyp = _arg(dy, torch.bfloat16, "dy", dev, (None, None))
+    xp = _arg(x, torch.bfloat16 if x_scales is None else torch.uint8, "x", dev, (None, None))
     (M_dy, N), (M_x, K) = dy.shape, x.shape
-    _arg(x_scales, torch.uint8, "x_scales", dev, (M_x, K // 32), optional=True)
-    _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
-    _arg(x_rows, torch.int32, "x_rows", dev, (None,), optional=True)
-    _arg(expert_offsets, torch.int32, "expert_offsets", dev, (None,))
-    E = int(expert_offsets.numel()) - 1
-    M_total = _m_total(M_total, dy_rows, x_rows)
-    if M_total is None:
-        M_total = min(M_dy, M_x)
+    sp = _arg(x_scales, torch.uint8, "x_scales", dev, (M_x, K // 32), optional=True)
+    drp = _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
+    xrp = _arg(x_rows, torch.int32, "x_rows", dev, (None,), optional=True)
+    op = _arg(expert_offsets, torch.int32, "expert_offsets", dev, (None,))
+    E = expert_offsets.shape[0] - 1
+    M_total = _m_total(M_total, min(M_dy, M_x), dy_rows, x_rows)
     if out is not None:
         dtype = out.dtype
     elif accumulate:
         raise NvfpError("accumulate needs out")
     if dtype not in (torch.float32, torch.bfloat16):
         raise NvfpError(f"dw must be float32 or bfloat16, not {dtype}")
-    _arg(out, dtype, "out", dev, (E, N, K), optional=True)
-    dw = out if out is not None else torch.empty((E, N, K), dtype=dtype, device=dev)
-    ws = _ws(_load().grouped_wgrad_workspace_size(E, M_total, N, K), dev)
-    _call("grouped_wgrad", dev, _ptr(dy), _ptr(dy_rows), M_dy, _ptr(x), _ptr(x_scales),
-          _ptr(x_rows), M_x, _ptr(expert_offsets), E, M_total, N, K, _ptr(dw),
-          int(dtype == torch.bfloat16), int(bool(accumulate)), _ptr(ws), ws.numel())
-    return dw
+    wp = _arg(out, dtype, "out", dev, (E, N, K), optional=True)
+    nb = (_lib or _load()).grouped_wgrad_workspace_size(E, M_total, N, K)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty((max(E, 0), N, K), dtype=dtype, device=dev)
+        wp = out.data_ptr()
+    _call("grouped_wgrad", dev, dyp, drp, M_dy, xp, sp, xrp, M_x, op, E, M_total, N, K, wp,
+          int(dtype is torch.bfloat16), int(bool(accumulate)), ws.data_ptr(), nb)
+    return out
 
 
 def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h=True):
@@ -688,21 +697,25 @@ def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h
     [T][tk] f32 as moe_permute returns them (both None: one slot per row,
     weight 1)."""
     dev = getattr(y, "device", None)
-    _arg(y, torch.bfloat16 if y_scales is None else torch.uint8, "y", dev, (None, None))
+    yp = _arg(y, torch.bfloat16 if y_scales is None else torch.uint8, "y", dev, (None, None))
     P, I2 = y.shape
     I = I2 // 2
     if I2 != 2 * I:
         raise NvfpError("y must be [gate | up]")
-    _arg(y_scales, torch.uint8, "y_scales", dev, (P, I2 // 32), optional=True)
-    _arg(dh, torch.bfloat16, "dh", dev, (P, I))
-    _arg(inv_perm, torch.int32, "inv_perm", dev, (None, None), optional=True)
+    sp = _arg(y_scales, torch.uint8, "y_scales", dev, (P, I2 // 32), optional=True)
+    dhp = _arg(dh, torch.bfloat16, "dh", dev, (P, I))
+    ip = _arg(inv_perm, torch.int32, "inv_perm", dev, (None, None), optional=True)
     T, tk = (P, 1) if inv_perm is None else inv_perm.shape
     if T * tk != P:
         raise NvfpError(f"inv_perm must have one entry for each of the {P} rows")
-    _arg(topk_w, torch.float32, "topk_w", dev, (T, tk), optional=True)
+    wp = _arg(topk_w, torch.float32, "topk_w", dev, (T, tk), optional=True)
     dy = torch.empty((P, I2), dtype=torch.bfloat16, device=dev)
-    hw = torch.empty((P, I), dtype=torch.bfloat16, device=dev) if want_h else None
-    dw = torch.empty((T, tk), dtype=torch.float32, device=dev) if topk_w is not None else None
-    _call("moe_swiglu_backward", dev, _ptr(y), _ptr(y_scales), _ptr(dh), _ptr(inv_perm),
-          _ptr(topk_w), T, tk, I, _ptr(dy), _ptr(hw), _ptr(dw))
+    hw = dw = hp = dwp = None
+    if want_h:
+        hw = torch.empty((P, I), dtype=torch.bfloat16, device=dev)
+        hp = hw.data_ptr()
+    if topk_w is not None:
+        dw = torch.empty((T, tk), dtype=torch.float32, device=dev)
+        dwp = dw.data_ptr()
+    _call("moe_swiglu_backward", dev, yp, sp, dhp, ip, wp, T, tk, I, dy.data_ptr(), hp, dwp)
     return dy, hw, dw
