@@ -28,7 +28,6 @@ struct GradArgs {
   int64_t M_dy, M_x, M_total, N, K;
   int E;
   int dw_bf16, accumulate;
-  int run;                     // wgrad: log2 of the tiles an XCD takes in a row
   int nsplit;                  // slices of the contraction
   float* part;                 // dgrad: their float32 parts [nsplit][M_total][K]
 };
@@ -595,27 +594,72 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   uint8_t* const stage[4] = {st0, st1, st2, st3};
 
   // ---- items -------------------------------------------------------------
-  const int per_e = n_tiles * m_tiles;
-  const int total = per_e * p.E;
-  const int items = total * p.nsplit;
-  const int xcd = (int)blockIdx.x & 7, loc = (int)blockIdx.x >> 3, per_xcd = (int)gridDim.x >> 3;
-  // the workgroup's i-th item: runs of 2^run items go to the XCDs in turn
-  // (workgroup b runs on XCD b % 8, each with its own L2), and an XCD's
-  // workgroups take its items in turn
-  auto item_at = [&](int i) __attribute__((always_inline)) {
-    const int j = loc + i * per_xcd;
-    return ((((j >> p.run) << 3) + xcd) << p.run) + (j & ((1 << p.run) - 1));
-  };
+  // expert by expert, tile by tile, slice by slice
+  const int per_tile = p.nsplit;
+  const int per_e = n_tiles * m_tiles * per_tile;
+  // Each XCD (workgroup b runs on XCD b % 8, each with its own L2) takes a
+  // contiguous range of the items, so that its workgroups share operands in
+  // L2, cut where an eighth of the work lies before it: an item costs its
+  // expert's steps (of the slice) and its stores.  (Runs of 32 items dealt to
+  // the XCDs in turn: 514 us against 492, 32768 rows over 128 experts, most
+  // of them with 50 to 1400 rows, 1536x2048 float32.)
+  int first, last;
+  {
+    int* const cost = reinterpret_cast<int*>(outb);   // [E], then their sums in front
+    int* const wsum = cost + 1024;
+    int mine[2], at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int ex = 2 * tid + i;
+      int64_t lo = 0, hi = 0;
+      if (ex < p.E) expert_rows(p, ex, lo, hi);
+      const int steps = (int)((hi - lo + BC - 1) / BC);
+      mine[i] = ex < p.E ? (steps + p.nsplit - 1) / p.nsplit + (p.dw_bf16 ? 6 : 11) : 0;
+    }
+    int sum = mine[0] + mine[1];
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (lane == 63) wsum[wave] = sum;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < 8; ++w) {
+      const int u = wsum[w];
+      if (w < wave) sum += u;
+      all += u;
+    }
+    at[0] = sum - mine[0] - mine[1];
+    at[1] = sum - mine[1];
+    // the expert that holds the cut writes the cut's item
+    const int x = (int)blockIdx.x & 7;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t cut = (int64_t)all * (x + c) / 8;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (mine[i] > 0 && cut >= at[i] && cut < at[i] + mine[i])
+          wsum[8 + c] = (2 * tid + i) * per_e + (int)((cut - at[i]) * per_e / mine[i]);
+    }
+    if (tid == 0 && x == 7) wsum[9] = p.E * per_e;
+    __syncthreads();
+    first = __builtin_amdgcn_readfirstlane(wsum[8]);
+    last = __builtin_amdgcn_readfirstlane(wsum[9]);
+    __syncthreads();
+  }
+  const int loc = (int)blockIdx.x >> 3, per_xcd = (int)gridDim.x >> 3;
+  // the workgroup's i-th item
+  auto item_at = [&](int i) __attribute__((always_inline)) { return first + loc + i * per_xcd; };
   struct Item {
     uint32_t lo, hi, a0, b0;
     int e, slice, steps;
   };
   auto item_of = [&](int v) __attribute__((always_inline)) {
     Item t;
-    t.slice = v / total;
-    v -= t.slice * total;
     t.e = v / per_e;
     v -= t.e * per_e;
+    t.slice = v % per_tile;
+    v /= per_tile;
     const int m = v / n_tiles;
     t.a0 = (uint32_t)m * kTile;
     t.b0 = (uint32_t)(v - m * n_tiles) * kTile;
@@ -634,9 +678,11 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     }
     t.lo = (uint32_t)lo;
     t.hi = (uint32_t)hi;
-    // a tile's steps are rounded up to the ring's four; the added ones load
-    // and multiply zeros
-    t.steps = (hi - lo + 4 * BC - 1) / (4 * BC) * 4;
+    // a tile's steps are rounded up to two; an added one loads and multiplies
+    // zeros (a tile that may end after any step has branches in each, across
+    // which instructions are not scheduled: 7% slower per step; rounding to
+    // the ring's four adds 1.5 steps to an average tile)
+    t.steps = (hi - lo + 2 * BC - 1) / (2 * BC) * 2;
     return t;
   };
 
@@ -646,13 +692,12 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   Item ahead;
   ahead.lo = ahead.hi = ahead.a0 = ahead.b0 = 0;
   ahead.steps = 0;
-  // (tiles begin at multiples of four: only there a new one can follow)
   auto next_step = [&](bool maybe_new) __attribute__((always_inline)) {
     ++ahead_s;
     while (maybe_new && ahead_s >= ahead.steps) {
       ahead_s = 0;
       const int v = item_at(++ahead_i);
-      if (v >= items) {   // none left: rows that are not there
+      if (v >= last) {   // none left: rows that are not there
         ahead.lo = ahead.hi = 0;
         ahead.steps = 1 << 30;
       } else {
@@ -795,7 +840,7 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
         }
         // nontemporal: dw is not read back soon, and its lines leave L2 to the
         // operands (wgrad of 32768 rows, 128 experts of 1536x2048: 0.52 ->
-        // 0.36 ms)
+        // 0.37 ms)
         __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, o, 0, 2);
       }
     };
@@ -835,10 +880,8 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   };
 
   // ---- the stream --------------------------------------------------------
-  load_ids(0, next_step(true));
-  load_ids(1, next_step(false));
-  load_ids(2, next_step(false));
-  load_ids(3, next_step(false));
+#pragma unroll
+  for (int u = 0; u < 4; ++u) load_ids(u, next_step(u % 2 == 0));
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     issue(stage[u], u);
@@ -848,30 +891,51 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   }
   wait_and_barrier<2 * kOps>();
   read(st0, 0);
-  bool stored = false;
-  auto body = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      read(stage[j], 1);
-      multiply(0);
-      if (j < 3 && stored) wait_and_barrier<2 * kOps + kStores>();
-      else wait_and_barrier<2 * kOps>();
-      read(stage[(j + 1) & 3], 0);
-      issue(stage[j], j);
-      load_ids((j + 2) & 3, next_step(j == 2));
-      fill(stage[(j + 2) & 3], (j + 2) & 3);
-      multiply(1);
-    }
-    stored = false;
+  int behind = 3;   // barriers since the last tile's stores
+  int i = 0, n = 0, v = item_at(0);
+  Item t;
+  bool done = v >= last;
+  if (!done) {
+    t = item_of(v);
+    n = t.steps;
+  }
+  clear();
+  // store the tile that ended, and those after it that have no rows
+  auto ended = [&]() __attribute__((always_inline)) {
+    do {
+      store(t);
+      clear();
+      behind = 0;
+      v = item_at(++i);
+      done = v >= last;
+      if (done) break;
+      t = item_of(v);
+      n = t.steps;
+    } while (n == 0);
   };
-  for (int i = 0;; ++i) {
-    const int v = item_at(i);
-    if (v >= items) break;
-    const Item t = item_of(v);
-    clear();
-    for (int s = 0; s < t.steps; s += 4) body();
-    store(t);
-    stored = true;
+  if (!done && n == 0) ended();
+  auto step = [&](auto j_c) __attribute__((always_inline)) {
+    constexpr int j = decltype(j_c)::value, j1 = (j + 1) & 3, j2 = (j + 2) & 3;
+    read(stage[j], 1);
+    multiply(0);
+    const WgStep next = next_step(j % 2 == 0);
+    if (behind < 3) wait_and_barrier<2 * kOps + kStores>();
+    else wait_and_barrier<2 * kOps>();
+    ++behind;
+    read(stage[j1], 0);
+    issue(stage[j], j);
+    load_ids(j2, next);
+    fill(stage[j2], j2);
+    multiply(1);
+  };
+  while (!done) {
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    if ((n -= 2) == 0) ended();
+    if (done) break;
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+    if ((n -= 2) == 0) ended();
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // fills past the end
 }
@@ -1067,9 +1131,6 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   const int64_t n_tiles = (K + kTile - 1) / kTile, m_tiles = (N + kTile - 1) / kTile;
   const int64_t items = E * n_tiles * m_tiles * p.nsplit;
   NV_REQUIRE(items < (1LL << 30), NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: more than 2^30 tiles");
-  // 32 tiles in a row keep an XCD's workgroups on one expert; fewer where the
-  // tiles would not reach every XCD a few times over
-  while (p.run < 5 && (512LL << p.run) <= items) ++p.run;
   const int64_t cus = num_cus() / 8 * 8 > 0 ? num_cus() / 8 * 8 : 8;
   const int64_t want = (items + 7) / 8 * 8;
   const unsigned grid = (unsigned)(want < cus ? want : cus);
