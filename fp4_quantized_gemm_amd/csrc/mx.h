@@ -16,14 +16,13 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t m) {
 
 __device__ __forceinline__ float mx_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// 8 codes times their scale -> 8 bf16 values, exact (4 significant bits)
+// 8 codes times their scale -> 8 bf16 values, exact (4 significant bits): one
+// hardware conversion per pair, which applies the scale's power of two
 __device__ __forceinline__ u32x4 mx_decode8(uint2 c, float s) {
-  const f32x2 v0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, false);
-  const f32x2 v1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.x, true);
-  const f32x2 v2 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, false);
-  const f32x2 v3 = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
-  return u32x4{pack_hi16(v0.x * s, v0.y * s), pack_hi16(v1.x * s, v1.y * s),
-               pack_hi16(v2.x * s, v2.y * s), pack_hi16(v3.x * s, v3.y * s)};
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, s, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.x, s, true)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, s, false)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c.y, s, true))};
 }
 
 }  // namespace nvfp4
