@@ -55,8 +55,8 @@ __device__ __forceinline__ int64_t source_row(const int32_t* rows, int64_t p, in
 // lane gets its column's four values.  16-byte chunk c of contraction row r
 // sits at c ^ swz(r): the four rows of a transposing load then lie in the four
 // 64-byte parts of the 256-byte bank line, and 16 rows of one chunk (the order
-// in which decoded weights are written) in 16 different 16-byte slots, so
-// neither conflicts.  bf16 operands go from memory to LDS directly; 4-bit
+// in which decoded weights are written) in 16 different 16-byte slots, eight
+// rows in eight different ones of a 128-byte half, so neither conflicts.  bf16 operands go from memory to LDS directly; 4-bit
 // weights and 8-bit activations are decoded (exactly) on the way, once per
 // workgroup.
 //
@@ -81,7 +81,9 @@ constexpr uint32_t kPastBuffer = 0xFFFFFFF0u;
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t* lds_tr_ptr;
 
-__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+__device__ __forceinline__ int swz(int r) {
+  return ((r & 3) << 2) | ((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1);
+}
 
 // 8 contraction values of one column: two transposing loads of 4 rows each
 __device__ __forceinline__ u32x4 tr_frag(const uint8_t* lo, const uint8_t* hi) {
@@ -333,12 +335,12 @@ k_dgrad(GradArgs p, int n_tiles) {
     constexpr int AU = decltype(au_c)::value, BU = decltype(bu_c)::value;
     read(sa[AU], sb[BU], 1);
     fill(sb[BU ^ 1], BU ^ 1, 0);
+    fill(sb[BU ^ 1], BU ^ 1, 1);
     multiply(0);
     read(sa[AU], sb[BU], 2);
-    fill(sb[BU ^ 1], BU ^ 1, 1);
+    fill(sb[BU ^ 1], BU ^ 1, 2);
     multiply(1);
     read(sa[AU], sb[BU], 3);
-    fill(sb[BU ^ 1], BU ^ 1, 2);
     fill(sb[BU ^ 1], BU ^ 1, 3);
     multiply(2);
     wait_and_barrier<6>();
@@ -458,7 +460,9 @@ k_dgrad_few(GradArgs p, int groups) {
   // the wave's [64][64] tile: 128-byte rows, chunk c of row r at c ^ wz(r):
   // four rows of a transposing load in four 64-byte bank parts, 16 rows of one
   // chunk (a write) in 16 slots
-  auto wz = [](int r) __attribute__((always_inline)) { return ((r & 2) << 1) | ((r >> 2) & 3); };
+  auto wz = [](int r) __attribute__((always_inline)) {
+    return ((r & 2) << 1) | ((r >> 1) & 2) | ((r ^ (r >> 3)) & 1);
+  };
   auto fill = [&](int set) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
