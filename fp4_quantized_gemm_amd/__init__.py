@@ -623,6 +623,8 @@ def _m_total(M_total, default, *row_lists):
                 M_total = n
             elif n < M_total:
                 raise NvfpError("a row list is shorter than M_total")
+    if M_total is not None and M_total < 0:
+        raise NvfpError("M_total must not be negative")
     return default if M_total is None else M_total
 
 

@@ -609,8 +609,7 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   // of them with 50 to 1400 rows, 1536x2048 float32.)
   int first, last;
   {
-    int* const cost = reinterpret_cast<int*>(outb);   // [E], then their sums in front
-    int* const wsum = cost + 1024;
+    int* const wsum = reinterpret_cast<int*>(outb);   // eight waves' sums, two cuts
     int mine[2], at[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -811,12 +810,13 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[half][j], fa[half][i], acc[i][j]);
-    // a matrix instruction, then up to two LDS reads, five others, one load
+    // a matrix instruction, then up to three LDS reads, four others, one load
+    // (two and five: 3% slower)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x006, 5, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+      __builtin_amdgcn_sched_group_barrier(0x006, 4, 0);
       __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
   };
@@ -1019,11 +1019,11 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
                         const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N,
                         int64_t K, void* dx, void* ws, size_t ws_bytes, void* stream) {
   NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 31) && M_src >= 0 &&
-                 N >= 16 && N % 16 == 0 && K >= 64 && K % 64 == 0 && N < (1LL << 31) &&
-                 K < (1LL << 31),
+                 N >= 16 && N % 16 == 0 && K >= 64 && K % 64 == 0 && N <= (1LL << 20) &&
+                 K <= (1LL << 20),
              NVFP4_ERR_SHAPE,
-             "grouped_w4a16_dgrad: need 1 <= E <= 1024, M_total < 2^31, N %% 16 == 0, K %% 64 == 0 "
-             "(E=%lld M_total=%lld N=%lld K=%lld)",
+             "grouped_w4a16_dgrad: need 1 <= E <= 1024, M_total < 2^31, N %% 16 == 0, K %% 64 == 0, "
+             "N and K up to 2^20 (E=%lld M_total=%lld N=%lld K=%lld)",
              (long long)E, (long long)M_total, (long long)N, (long long)K);
   NV_REQUIRE(dy_rows != nullptr || M_src >= M_total, NVFP4_ERR_SHAPE,
              "grouped_w4a16_dgrad: without dy_rows, M_src must be >= M_total");
@@ -1090,11 +1090,11 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
                   const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
                   void* dw, int dw_bf16, int accumulate, void* ws, size_t ws_bytes, void* stream) {
   NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 30) && M_dy >= 0 &&
-                 M_x >= 0 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 && N < (1LL << 31) &&
-                 K < (1LL << 31) && (x_scales == nullptr || K % 32 == 0),
+                 M_x >= 0 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 && N <= (1LL << 20) &&
+                 K <= (1LL << 20) && (x_scales == nullptr || K % 32 == 0),
              NVFP4_ERR_SHAPE,
              "grouped_wgrad: need 1 <= E <= 1024, M_total < 2^30, N %% 8 == 0, K %% 8 == 0 "
-             "(K %% 32 == 0 for 8-bit x) (E=%lld M_total=%lld N=%lld K=%lld)",
+             "(K %% 32 == 0 for 8-bit x), N and K up to 2^20 (E=%lld M_total=%lld N=%lld K=%lld)",
              (long long)E, (long long)M_total, (long long)N, (long long)K);
   NV_REQUIRE((dy_rows != nullptr || M_dy >= M_total) && (x_rows != nullptr || M_x >= M_total),
              NVFP4_ERR_SHAPE, "grouped_wgrad: an operand without a row list needs M_total rows");

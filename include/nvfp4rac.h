@@ -418,9 +418,12 @@ int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * w~ = e2m1 * e4m3 exact in bf16, float32 accumulation, one rounding.  dx
  * [M_total][K] bf16; rows outside [off[0], off[E]) are left as they were.
  * The weights are the packed copy the forward takes.  Same rules for the
- * expert grouping as grouped_w4a16_gemm.  Requires 1 <= E <= 1024,
- * M_total < 2^31, N % 16 == 0, K % 64 == 0, M_src * N * 2 < 2^32,
- * N * K / 2 < 2^32; dy_rows == NULL needs M_src >= M_total. */
+ * expert grouping as grouped_w4a16_gemm; dx overlaps no input.  The workspace
+ * holds a tile prefix and, where the tiles fill less than the chip, float32
+ * parts of up to 16 slices of n, summed in slice order.  Requires
+ * 1 <= E <= 1024, M_total < 2^31, N % 16 == 0, K % 64 == 0, N and K <= 2^20,
+ * M_src * N * 2 < 2^32, N * K / 2 < 2^32; dy_rows == NULL needs
+ * M_src >= M_total. */
 size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
                         const uint8_t* w_codes, const uint8_t* w_scales, const float* g_w,
@@ -435,9 +438,12 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
  * they stand for.  Float32 accumulation in an order that does not depend on
  * timing.  dw [E][N][K]: float32, or bf16 with dw_bf16 = 1 (one rounding); an
  * expert without rows gets zeros.  accumulate = 1 (float32 only): the sum is
- * added to what dw holds.  Requires 1 <= E <= 1024, M_total < 2^30,
- * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), N * K < 2^30,
- * M_dy * N * 2 < 2^32, x below 4 GiB; an operand without a row list has at least M_total rows. */
+ * added to what dw holds; dw overlaps no input.  The workspace holds, where
+ * the tiles fill less than the chip, float32 parts of up to 64 slices of the
+ * rows, summed in slice order.  Requires 1 <= E <= 1024, M_total < 2^30,
+ * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), N and K <= 2^20,
+ * N * K < 2^30, M_dy * N * 2 < 2^32, x below 4 GiB; an operand without a row
+ * list has at least M_total rows. */
 size_t grouped_wgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const void* x,
                   const uint8_t* x_scales, const int32_t* x_rows, int64_t M_x,

@@ -42,7 +42,8 @@ def dgrad(dy=A, rows=A, M=64, wc=A, ws=A, g=A, off=A, E=2, P=128, N=64, K=128, d
 
 @pytest.mark.parametrize("kw,want", [
     (dict(E=0), ERR_SHAPE), (dict(E=1025), ERR_SHAPE), (dict(N=24), ERR_SHAPE),
-    (dict(K=96), ERR_SHAPE), (dict(P=-1), ERR_SHAPE), (dict(P=1 << 31), ERR_SHAPE),
+    (dict(K=96), ERR_SHAPE), (dict(N=(1 << 20) + 16, M=1, P=1), ERR_SHAPE),
+    (dict(K=(1 << 20) + 64), ERR_SHAPE), (dict(P=-1), ERR_SHAPE), (dict(P=1 << 31), ERR_SHAPE),
     (dict(rows=None), ERR_SHAPE),                       # 64 rows for 128
     (dict(M=0), ERR_SHAPE), (dict(M=-3), ERR_SHAPE),
     (dict(M=1 << 26), ERR_UNSUP),                       # dy of 8 GiB
@@ -69,7 +70,8 @@ def wgrad(dy=A, dyr=None, Md=128, x=A, xs=None, xr=None, Mx=128, off=A, E=2, P=1
     (dict(Md=127), ERR_SHAPE), (dict(Mx=127), ERR_SHAPE),
     (dict(Md=0, dyr=A), ERR_SHAPE), (dict(Mx=0, xr=A), ERR_SHAPE),
     (dict(Md=1 << 25), ERR_UNSUP), (dict(Mx=1 << 25), ERR_UNSUP),
-    (dict(Mx=1 << 26, xs=A), ERR_UNSUP),
+    (dict(Mx=1 << 26, xs=A), ERR_UNSUP), (dict(P=1 << 30, Md=1 << 30, Mx=1 << 30), ERR_SHAPE),
+    (dict(N=(1 << 20) + 8), ERR_SHAPE), (dict(N=1 << 16, K=1 << 14), ERR_UNSUP),
     (dict(bf=2), ERR_UNSUP), (dict(bf=1, acc=1), ERR_UNSUP),
     (dict(dy=None), ERR_NULL), (dict(x=None), ERR_NULL), (dict(off=None), ERR_NULL),
     (dict(dw=None), ERR_NULL), (dict(w=None), ERR_NULL),

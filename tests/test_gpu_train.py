@@ -251,6 +251,27 @@ def test_dgrad_zero_weights_and_no_rows(dev):
     assert dx.shape == (0, 128)
 
 
+def test_dgrad_many_experts(dev):
+    """1024 experts, most without rows, the first rows of the permutation in
+    none of them; few rows per expert and, on 40 experts, many."""
+    for E, top, N, K in [(1024, 6, 32, 64), (40, 200, 48, 320)]:
+        say(f"dgrad E={E}")
+        rng = np.random.default_rng(E)
+        counts = np.where(rng.random(E) < 0.5, 0, rng.integers(0, top, E))
+        offs = offsets_of(counts) + 7
+        P = int(offs[-1])
+        dy = heavy_bf16(rng, (P, N)) * 2.0 ** -10
+        w = OF.round_to_bf16(rng.standard_normal((E, N, K)) * 0.02)
+        wc, ws, gw, _ = OQ.qdq_weights(w)
+        out = torch.full((P, K), 5.0, dtype=torch.bfloat16, device="cuda")
+        run_dgrad(dy, None, wc, ws, gw, offs, out=out)
+        torch.cuda.synchronize()
+        ref, mag = OT.grouped_dgrad(dy, None, wc, ws, gw, offs)
+        got = host_vals(out)
+        assert np.all(got[:7] == 5.0)
+        check_dgrad(got[7:], ref[7:], mag[7:], N, "dx")
+
+
 # ------------------------------------------------------------ weight gradient
 WGRAD = [
     ([1], 8, 8),
@@ -343,6 +364,64 @@ def test_wgrad_keeps_other_rows_out(dev, fp8):
     assert bad[3].all() and bad[:, 4].all()
     bad[3], bad[:, 4] = False, False
     assert not bad.any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("E,N,K,top", [(40, 520, 800, 140), (1024, 16, 32, 5), (7, 1800, 2080, 90)])
+def test_wgrad_more_tiles_than_workgroups(dev, E, N, K, top, fp8):
+    """Several tiles per workgroup, of different lengths and without rows in
+    any order; rows before the first expert belong to none."""
+    say(f"wgrad E={E} N={N} K={K} fp8={fp8}")
+    rng = np.random.default_rng(E + N)
+    counts = np.where(rng.random(E) < 0.3, 0, rng.integers(0, top, E))
+    offs = offsets_of(counts) + 3
+    P = int(offs[-1])
+    dy, x = heavy_bf16(rng, (P, N)) * 2.0 ** -10, heavy_bf16(rng, (P, K))
+    xd, xs = dev_vals(x), None
+    if fp8:
+        codes, scales = OT.mxfp8_encode(x)
+        x, xd, xs = OT.mxfp8_value(codes, scales), cu(codes), cu(scales)
+    dyd, o = dev_vals(dy), cu(offs)
+    dw = F.grouped_wgrad(dyd, None, xd, None, o, x_scales=xs)
+    db = F.grouped_wgrad(dyd, None, xd, None, o, x_scales=xs, dtype=torch.bfloat16)
+    acc = F.grouped_wgrad(dyd, None, xd, None, o, x_scales=xs, out=torch.ones_like(dw),
+                          accumulate=True)
+    torch.cuda.synchronize()
+    ref, mag = OT.grouped_wgrad(dy, None, x, None, offs)
+    lim = max(counts) * U * mag + TINY
+    check(dw.cpu().numpy().astype(np.float64), ref, lim, "dw")
+    check(host_vals(db), ref, np.abs(ref) * 2.0 ** -8 + lim, "dw bf16")
+    check(acc.cpu().numpy().astype(np.float64), ref + 1, lim + U * (np.abs(ref + 1) + lim), "added")
+
+
+def test_gradients_of_operands_near_4_gib(dev):
+    """Gathered rows behind the 2 and 4 GiB marks of dy (and of x): the same
+    bits as from small tensors."""
+    say("near 4 GiB")
+    rng = np.random.default_rng(9)
+    M, N, n = 524000, 4096, 300                          # 4292608000 bytes
+    small = dev_vals(heavy_bf16(rng, (n, N)))
+    big = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+    rows = torch.from_numpy(np.sort(rng.choice(M, n, replace=False))).cuda()
+    rows[-1], rows[0] = M - 1, 0
+    big[rows] = small
+    order = torch.from_numpy(rng.permutation(n)).cuda()
+    offs = cu(np.array([0, 20, 300], np.int32))
+    far, near = rows[order].int(), order.int()
+    w = F.nvfp4_qdq_weights(dev_vals(OF.round_to_bf16(rng.standard_normal((2, N, 128)) * 0.02)),
+                            want_qdq=False)
+    W = (w.packed_codes, w.packed_scales, w.g)
+    for M_total in (300, 20):                            # both kernels
+        o = offs.clamp(max=M_total)
+        a = F.grouped_w4a16_dgrad(big, far, *W, o, M_total=M_total)
+        b = F.grouped_w4a16_dgrad(small, near, *W, o, M_total=M_total)
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    other = dev_vals(heavy_bf16(rng, (n, 64)))
+    for dy, dyr, dys, dysr, x, xr, xs, xsr in [(big, far, small, near, other, None, other, None),
+                                               (other, None, other, None, big, far, small, near)]:
+        a = F.grouped_wgrad(dy, dyr, x, xr, offs)
+        b = F.grouped_wgrad(dys, dysr, xs, xsr, offs)
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
 
 
 def test_wgrad_no_rows(dev):
@@ -573,6 +652,8 @@ def test_binding_refusals(dev):
         F.grouped_w4a16_dgrad(b, rows, *W, offs, M_total=5)
     with pytest.raises(F.NvfpError, match="M_src"):
         F.grouped_w4a16_dgrad(b, None, *W, offs, M_total=5)
+    with pytest.raises(F.NvfpError, match="negative"):
+        F.grouped_w4a16_dgrad(b, rows, *W, offs, M_total=-1)
     with pytest.raises(F.NvfpError, match="contiguous"):
         F.grouped_w4a16_dgrad(torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")[:, ::2],
                               None, *W, offs)
