@@ -634,8 +634,9 @@ def grouped_w4a16_dgrad(dy, dy_rows, w_codes, w_scales, g_w, expert_offsets, M_t
     the dequantized NVFP4 weights of each row's expert, contracted over N: the
     input gradient of grouped_w4a16_gemm.  Rows outside the experts' are left
     as they were."""
-    dev = getattr(dy, "device", None)
-    _arg(dy, torch.bfloat16, "dy", dev, (None, None))
+    if not isinstance(dy, torch.Tensor) or not dy.is_cuda:
+        raise NvfpError("dy must be a device tensor")
+    dev = dy.device
     E, N = _wshape(w_codes)
     K = w_codes.shape[3] * 64
     dyp = _arg(dy, torch.bfloat16, "dy", dev, (None, N))

@@ -172,7 +172,7 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // the weights as [64][256] in two, decoded one step ahead from registers
 // loaded two steps earlier.  Where the tiles fill less than the chip the
 // contraction is split: each slice writes its float32 part (times g_w), and
-// k_dgrad_join adds them in slice order.
+// k_dgrad_join adds them.
 // ---------------------------------------------------------------------------
 namespace dg {
 constexpr int BC = 64;
@@ -480,7 +480,7 @@ k_dgrad_few(GradArgs p, int groups) {
   const uint32_t t_off1 = (t_row + 4) * 128 + ((t_chunk ^ wz(t_row + 4)) << 4) + (lane & 1) * 8;
   const float sc = p.g_w[e];
 
-  for (int64_t r0 = lo; r0 < hi; r0 += 32) {
+  for (int64_t r0 = lo + 32 * (int64_t)blockIdx.y; r0 < hi; r0 += 32 * (int64_t)gridDim.y) {
     const int64_t pr = r0 + r32;
     const uint32_t off_a =
         pr < hi ? (uint32_t)source_row(p.dy_rows, pr, p.M_dy) * N2 + 16u * kg : kPastBuffer;
@@ -528,20 +528,47 @@ k_dgrad_few(GradArgs p, int groups) {
   }
 }
 
-// dx = sum of the slices' parts, in slice order, over the experts' rows; four
-// columns per lane
+// Sum over the slices of four elements at q of parts of n each: G groups of
+// 256 / G lanes take a G-th of the slices each, and their sums are added in
+// order.  Group 0 gets the sum.  (One group over 64 slices of 5120 elements:
+// 40 us, as its loads wait for one another.)
+template <int G>
+__device__ __forceinline__ f32x4 slice_sum(const float* __restrict__ part, int64_t q, int64_t n,
+                                           int nsplit, bool there) {
+  const int g = threadIdx.x / (256 / G), lane = threadIdx.x % (256 / G);
+  const int per = (nsplit + G - 1) / G;
+  const int end = (g + 1) * per < nsplit ? (g + 1) * per : nsplit;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (there) {
+#pragma unroll 4
+    for (int i = g * per; i < end; ++i) s += *reinterpret_cast<const f32x4*>(part + i * n + q);
+  }
+  if constexpr (G > 1) {
+    __shared__ f32x4 sums[G][256 / G];
+    sums[g][lane] = s;
+    __syncthreads();
+    s = sums[0][lane];
+#pragma unroll
+    for (int i = 1; i < G; ++i) s += sums[i][lane];
+    __syncthreads();
+  }
+  return s;
+}
+
+// dx = sum of the slices' parts over the experts' rows; four columns per lane
+template <int G>
 __global__ void __launch_bounds__(256)
 k_dgrad_join(const float* __restrict__ part, const int32_t* __restrict__ offsets, int E,
              int64_t M_total, int64_t K, int nsplit, uint16_t* __restrict__ dx) {
+  constexpr int L = 256 / G;
   int64_t lo = offsets[0], hi = offsets[E];
   lo = lo < 0 ? 0 : lo;
-  hi = hi > M_total ? M_total : hi;
-  const int64_t n = M_total * K;
-  for (int64_t q = lo * K + (blockIdx.x * 256LL + threadIdx.x) * 4; q < hi * K;
-       q += gridDim.x * 1024LL) {
-    f32x4 s = *reinterpret_cast<const f32x4*>(part + q);
-    for (int i = 1; i < nsplit; ++i) s += *reinterpret_cast<const f32x4*>(part + i * n + q);
-    *reinterpret_cast<uint2*>(dx + q) = make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
+  hi = (hi > M_total ? M_total : hi) * K;
+  for (int64_t q0 = lo * K + blockIdx.x * (4LL * L); q0 < hi; q0 += gridDim.x * (4LL * L)) {
+    const int64_t q = q0 + (threadIdx.x % L) * 4;
+    const f32x4 s = slice_sum<G>(part, q, M_total * K, nsplit, q < hi);
+    if (threadIdx.x < L && q < hi)
+      *reinterpret_cast<uint2*>(dx + q) = make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
   }
 }
 
@@ -962,7 +989,8 @@ static int dgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
   if (dgrad_few_rows(E, M_total)) {
     s = 4096 / ((E < M_total ? E : (M_total < 1 ? 1 : M_total)) * (K / 64));
   } else {
-    s = 256 / ((M_total + kTile - 1) / kTile * ((K + kTile - 1) / kTile));
+    // (an expert's last tile is half full on average)
+    s = 256 / (((M_total + kTile - 1) / kTile + E / 2) * ((K + kTile - 1) / kTile));
   }
   s = s > steps / 8 ? steps / 8 : s;
   s = s < 1 ? 1 : (s > 16 ? 16 : s);
@@ -970,14 +998,16 @@ static int dgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
   return (int)((steps + per - 1) / per);   // no slice is empty
 }
 
-// dw = sum of the slices' partial products, in slice order; 4 per lane
-template <bool BF16>
+// dw = sum of the slices' partial products; four elements per lane
+template <int G, bool BF16>
 __global__ void __launch_bounds__(256)
 k_wgrad_reduce(const float* __restrict__ part, int64_t n, int nsplit, void* __restrict__ dw,
                int accumulate) {
-  for (int64_t q = (blockIdx.x * 256LL + threadIdx.x) * 4; q < n; q += gridDim.x * 1024LL) {
-    f32x4 s = *reinterpret_cast<const f32x4*>(part + q);
-    for (int i = 1; i < nsplit; ++i) s += *reinterpret_cast<const f32x4*>(part + i * n + q);
+  constexpr int L = 256 / G;
+  for (int64_t q0 = blockIdx.x * (4LL * L); q0 < n; q0 += gridDim.x * (4LL * L)) {
+    const int64_t q = q0 + (threadIdx.x % L) * 4;
+    const f32x4 s = slice_sum<G>(part, q, n, nsplit, q < n);
+    if (threadIdx.x >= L || q >= n) continue;
     if constexpr (BF16) {
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dw) + q) =
           make_uint2(bf16x2_rne(s.x, s.y), bf16x2_rne(s.z, s.w));
@@ -986,6 +1016,12 @@ k_wgrad_reduce(const float* __restrict__ part, int64_t n, int nsplit, void* __re
       *d = accumulate ? *d + s : s;
     }
   }
+}
+
+// workgroups of a slice sum over n elements with G groups
+static unsigned join_grid(int64_t n, int G) {
+  const int64_t per = 1024 / G, g = (n + per - 1) / per;
+  return (unsigned)(g < 65536 ? g : 65536);
 }
 
 // Slices of each expert's rows for a weight gradient whose tiles fill less
@@ -1061,7 +1097,9 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
     const int64_t blocks = E * groups * p.nsplit;
     NV_REQUIRE(blocks < (1LL << 23), NVFP4_ERR_UNSUPPORTED,
                "grouped_w4a16_dgrad: more than 2^23 tiles");
-    k_dgrad_few<<<(unsigned)blocks, 256, 0, s>>>(p, (int)groups);
+    // (33 to 64 rows in all: the two passes an expert may need side by side)
+    k_dgrad_few<<<dim3((unsigned)blocks, M_total > 32 && M_total <= 64 ? 2 : 1), 256, 0, s>>>(
+        p, (int)groups);
   } else {
     const int64_t n_tiles = (K + kTile - 1) / kTile;
     const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
@@ -1072,9 +1110,12 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
     k_dgrad<<<dim3((unsigned)blocks, (unsigned)p.nsplit), 512, 0, s>>>(p, (int)n_tiles);
   }
   if (p.nsplit > 1) {
-    const int64_t g = (M_total * K + 1023) / 1024;
-    k_dgrad_join<<<(unsigned)(g < 65536 ? g : 65536), 256, 0, s>>>(
-        p.part, expert_offsets, (int)E, M_total, K, p.nsplit, p.dx);
+    if (p.nsplit >= 8)
+      k_dgrad_join<4><<<join_grid(M_total * K, 4), 256, 0, s>>>(p.part, expert_offsets, (int)E,
+                                                                M_total, K, p.nsplit, p.dx);
+    else
+      k_dgrad_join<1><<<join_grid(M_total * K, 1), 256, 0, s>>>(p.part, expert_offsets, (int)E,
+                                                                M_total, K, p.nsplit, p.dx);
   }
   return check_launch("grouped_w4a16_dgrad");
 }
@@ -1152,13 +1193,16 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
   k<<<grid, 512, 0, s>>>(p, nt, mt);
   if (split) {
     const int64_t n = E * N * K;
-    const int64_t g = (n + 1023) / 1024;
-    const unsigned rg = (unsigned)(g < 65536 ? g : 65536);
-    if (dw_bf16)
-      k_wgrad_reduce<true><<<rg, 256, 0, s>>>(static_cast<float*>(ws), n, p.nsplit, dw, 0);
+    const float* part = static_cast<const float*>(ws);
+    const int ns = p.nsplit, add = accumulate != 0;
+    if (dw_bf16 && ns >= 8)
+      k_wgrad_reduce<4, true><<<join_grid(n, 4), 256, 0, s>>>(part, n, ns, dw, 0);
+    else if (dw_bf16)
+      k_wgrad_reduce<1, true><<<join_grid(n, 1), 256, 0, s>>>(part, n, ns, dw, 0);
+    else if (ns >= 8)
+      k_wgrad_reduce<4, false><<<join_grid(n, 4), 256, 0, s>>>(part, n, ns, dw, add);
     else
-      k_wgrad_reduce<false><<<rg, 256, 0, s>>>(static_cast<float*>(ws), n, p.nsplit, dw,
-                                               accumulate != 0);
+      k_wgrad_reduce<1, false><<<join_grid(n, 1), 256, 0, s>>>(part, n, ns, dw, add);
   }
   return check_launch("grouped_wgrad");
 }

@@ -420,7 +420,7 @@ int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * The weights are the packed copy the forward takes.  Same rules for the
  * expert grouping as grouped_w4a16_gemm; dx overlaps no input.  The workspace
  * holds a tile prefix and, where the tiles fill less than the chip, float32
- * parts of up to 16 slices of n, summed in slice order.  Requires
+ * parts of up to 16 slices of n, summed in a fixed order.  Requires
  * 1 <= E <= 1024, M_total < 2^31, N % 16 == 0, K % 64 == 0, N and K <= 2^20,
  * M_src * N * 2 < 2^32, N * K / 2 < 2^32; dy_rows == NULL needs
  * M_src >= M_total. */
@@ -440,7 +440,7 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
  * expert without rows gets zeros.  accumulate = 1 (float32 only): the sum is
  * added to what dw holds; dw overlaps no input.  The workspace holds, where
  * the tiles fill less than the chip, float32 parts of up to 64 slices of the
- * rows, summed in slice order.  Requires 1 <= E <= 1024, M_total < 2^30,
+ * rows, summed in a fixed order.  Requires 1 <= E <= 1024, M_total < 2^30,
  * N % 8 == 0, K % 8 == 0 (K % 32 == 0 with x_scales), N and K <= 2^20,
  * N * K < 2^30, M_dy * N * 2 < 2^32, x below 4 GiB; an operand without a row
  * list has at least M_total rows. */
