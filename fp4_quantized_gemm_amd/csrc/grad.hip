@@ -173,6 +173,16 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // loaded two steps earlier.  Where the tiles fill less than the chip the
 // contraction is split: each slice writes its float32 part (times g_w), and
 // k_dgrad_join adds them.
+//
+// A row tile of an expert's last 128 (64) rows or fewer is multiplied with 64
+// (32) rows per wave: it costs its weights' decode, not a full tile's products
+// (2048 rows over 128 experts 275 -> 207 us).  Measured: 131072 rows,
+// 128 experts of 4096x1536, 1.53 ms = 1.08 PFLOP/s; 32768 rows, 128 experts of
+// 1536x2048 (half the experts a tile and a tail), 0.28 ms.  Without the weight
+// decode the first took 1.30 instead of 1.59 ms; matrix units 53% busy, at
+// 1.8 GHz: the chip's power limit, then LDS and vector instructions beside the
+// products.  A persistent form (one workgroup per CU) was slower, 1.57 ms and
+// 0.31 ms.
 // ---------------------------------------------------------------------------
 namespace dg {
 constexpr int BC = 64;
@@ -298,89 +308,89 @@ k_dgrad(GradArgs p, int n_tiles) {
   // the tile with NV 32-row blocks per row of waves; whole, so that no
   // accumulator is merged between variants
   auto whole = [&](auto nv_c) __attribute__((always_inline)) {
-  constexpr int NV = decltype(nv_c)::value;
-  f32x16_t acc[NV][2];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const uint32_t a_row = (wm * 32 * NV + r32) * 128;
-  u32x4 fa[2][NV], fb[2][2];   // by slice % 2
-  auto read = [&](const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) fb[s & 1][j] = tr.at(b + s * 8192, 2 * wn + j);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      fa[s & 1][i] = *reinterpret_cast<const u32x4*>(a + a_row + 32 * i * 128 +
-                                                     (((2 * s + kg) ^ a_sw) << 4));
-  };
-  auto multiply = [&](int s) __attribute__((always_inline)) {
+    constexpr int NV = decltype(nv_c)::value;
+    f32x16_t acc[NV][2];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
-    // a matrix instruction, then LDS reads, vector instructions, a load
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int i = 0; i < 2 * NV; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, NV == 4 ? 1 : NV == 2 ? 2 : 3, 0);
-      __builtin_amdgcn_sched_group_barrier(0x006, NV == 4 ? 5 : 10, 0);
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const uint32_t a_row = (wm * 32 * NV + r32) * 128;
+    u32x4 fa[2][NV], fb[2][2];   // by slice % 2
+    auto read = [&](const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fb[s & 1][j] = tr.at(b + s * 8192, 2 * wn + j);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        fa[s & 1][i] = *reinterpret_cast<const u32x4*>(a + a_row + 32 * i * 128 +
+                                                       (((2 * s + kg) ^ a_sw) << 4));
+    };
+    auto multiply = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma32_bf16(fb[s & 1][j], fa[s & 1][i], acc[i][j]);
+      // a matrix instruction, then LDS reads, vector instructions, a load
+#pragma unroll
+      for (int i = 0; i < 2 * NV; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, NV == 4 ? 1 : NV == 2 ? 2 : 3, 0);
+        __builtin_amdgcn_sched_group_barrier(0x006, NV == 4 ? 5 : 10, 0);
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+      }
+    };
+    // step u: dy stage AU, weight stage BU
+    auto step = [&](auto au_c, auto bu_c, int u) __attribute__((always_inline)) {
+      constexpr int AU = decltype(au_c)::value, BU = decltype(bu_c)::value;
+      read(sa[AU], sb[BU], 1);
+      fill(sb[BU ^ 1], BU ^ 1, 0);
+      fill(sb[BU ^ 1], BU ^ 1, 1);
+      multiply(0);
+      read(sa[AU], sb[BU], 2);
+      fill(sb[BU ^ 1], BU ^ 1, 2);
+      multiply(1);
+      read(sa[AU], sb[BU], 3);
+      fill(sb[BU ^ 1], BU ^ 1, 3);
+      multiply(2);
+      wait_and_barrier<6>();
+      issue_w(BU ^ 1, u + 3);
+      issue_a(sa[AU], u + 3);
+      read(sa[(AU + 1) % 3], sb[BU ^ 1], 0);
+      multiply(3);
+    };
+    read(sa0, sb0, 0);
+    using c0 = std::integral_constant<int, 0>;
+    using c1 = std::integral_constant<int, 1>;
+    using c2 = std::integral_constant<int, 2>;
+    for (int u = u0; u < u1;) {
+      step(c0{}, c0{}, u);
+      if (++u >= u1) break;
+      step(c1{}, c1{}, u);
+      if (++u >= u1) break;
+      step(c2{}, c0{}, u);
+      if (++u >= u1) break;
+      step(c0{}, c1{}, u);
+      if (++u >= u1) break;
+      step(c1{}, c0{}, u);
+      if (++u >= u1) break;
+      step(c2{}, c1{}, u);
+      if (++u >= u1) break;
     }
-  };
-  // step u: dy stage AU, weight stage BU
-  auto step = [&](auto au_c, auto bu_c, int u) __attribute__((always_inline)) {
-    constexpr int AU = decltype(au_c)::value, BU = decltype(bu_c)::value;
-    read(sa[AU], sb[BU], 1);
-    fill(sb[BU ^ 1], BU ^ 1, 0);
-    fill(sb[BU ^ 1], BU ^ 1, 1);
-    multiply(0);
-    read(sa[AU], sb[BU], 2);
-    fill(sb[BU ^ 1], BU ^ 1, 2);
-    multiply(1);
-    read(sa[AU], sb[BU], 3);
-    fill(sb[BU ^ 1], BU ^ 1, 3);
-    multiply(2);
-    wait_and_barrier<6>();
-    issue_w(BU ^ 1, u + 3);
-    issue_a(sa[AU], u + 3);
-    read(sa[(AU + 1) % 3], sb[BU ^ 1], 0);
-    multiply(3);
-  };
-  read(sa0, sb0, 0);
-  using c0 = std::integral_constant<int, 0>;
-  using c1 = std::integral_constant<int, 1>;
-  using c2 = std::integral_constant<int, 2>;
-  for (int u = u0; u < u1;) {
-    step(c0{}, c0{}, u);
-    if (++u >= u1) break;
-    step(c1{}, c1{}, u);
-    if (++u >= u1) break;
-    step(c2{}, c0{}, u);
-    if (++u >= u1) break;
-    step(c0{}, c1{}, u);
-    if (++u >= u1) break;
-    step(c1{}, c0{}, u);
-    if (++u >= u1) break;
-    step(c2{}, c1{}, u);
-    if (++u >= u1) break;
-  }
-  wait_and_barrier<0>();
+    wait_and_barrier<0>();
 
-  const float sc = p.g_w[e];
-  const int64_t rows = hi - a0 < kTile ? hi - a0 : kTile;
+    const float sc = p.g_w[e];
+    const int64_t rows = hi - a0 < kTile ? hi - a0 : kTile;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t r0 = 32 * (NV * wm + i), k0 = (uint32_t)b0 + 64 * wn;
-    if (p.nsplit == 1)
-      dgrad_out(sa0 + wave * 4096, acc[i], sc, p.dx + a0 * p.K, rows, r0, k0, (uint32_t)p.K);
-    else
-      dgrad_out(sa0 + wave * 4096, acc[i], sc,
-                p.part + ((int64_t)blockIdx.y * p.M_total + a0) * p.K, rows, r0, k0,
-                (uint32_t)p.K);
-  }
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t r0 = 32 * (NV * wm + i), k0 = (uint32_t)b0 + 64 * wn;
+      if (p.nsplit == 1)
+        dgrad_out(sa0 + wave * 4096, acc[i], sc, p.dx + a0 * p.K, rows, r0, k0, (uint32_t)p.K);
+      else
+        dgrad_out(sa0 + wave * 4096, acc[i], sc,
+                  p.part + ((int64_t)blockIdx.y * p.M_total + a0) * p.K, rows, r0, k0,
+                  (uint32_t)p.K);
+    }
   };
   if (hi - a0 > 128) whole(std::integral_constant<int, 4>{});
   else if (hi - a0 > 64) whole(std::integral_constant<int, 2>{});
@@ -395,6 +405,12 @@ k_dgrad(GradArgs p, int n_tiles) {
 // through the transposing load; dy's fragments come from memory (the four
 // waves of a workgroup, four strips of one expert, share them in L1).  32 rows
 // of the expert per pass; more re-stream the weights.
+//
+// Measured: 2048 rows over 128 experts of 4096x1536, 115 us = 4.0 TB/s of
+// weights (207 us tile by tile); one row of one such expert 20 us.  Bound by
+// its vector instructions (two per decoded weight, 16 per 8) and their issue,
+// with three waves per SIMD; with up to 64 rows per pass and two waves per SIMD
+// 146 us.
 // ---------------------------------------------------------------------------
 namespace dgf {
 constexpr int BC = 64;
@@ -601,6 +617,13 @@ struct WgStep {
   uint32_t p, hi, a0, b0;
 };
 
+// Measured: 131072 rows, 128 experts of 4096x1536, bf16 dw, 1.54 ms = 1.07
+// PFLOP/s (1.35 ms without the stores; 0.97 ms with operands of zeros, at the
+// full clock): bound by the chip's power limit at these operands (1.5 to 1.7
+// GHz, matrix units 64% busy).  32768 rows from 8-bit x, 128 experts of
+// 1536x2048, float32 dw (1.6 GB), 0.48 ms, 0.25 ms without the stores: bound by
+// the stores (5.5 TB/s with nothing else running) and operands that come from
+// memory beside them.
 // MX: x is an 8-bit checkpoint.  LA, LB: dy, x are gathered through a row list
 // (without one a row is its step's own, and no per-row arithmetic is left).
 template <bool MX, bool LA, bool LB>

