@@ -130,8 +130,8 @@ def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeigh
     """The block with the trainer's W4A16 products (bf16 activations): x [T][H]
     bf16, logits [T][E] f32, w_first [E][2I][H], w_down [E][H][I] -> (out
     [T][H] bf16, TrainState).  checkpoint="mxfp8" keeps x and the gate and up
-    products in 8 bits (2.06 bytes per element of both together instead of 4),
-    "bf16" keeps them as they are."""
+    products in 8 bits (1.03 bytes per element instead of 2), "bf16" keeps
+    them as they are."""
     if checkpoint not in ("mxfp8", "bf16"):
         raise ValueError(f"checkpoint must be 'mxfp8' or 'bf16', not {checkpoint!r}")
     mx = checkpoint == "mxfp8"

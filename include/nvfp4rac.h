@@ -463,7 +463,7 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
  *   d_topk_w[t][j] = sum_i dh_i gate_i s_i up_i   float32 [T][tk] or NULL
  * The gradient of the routing logits follows from d_topk_w as that of a
  * softmax over the tk chosen experts.  inv_perm is a permutation; an entry
- * outside [0, T*tk) is skipped.  Requires 1 <= tk <= 32, T*tk < 2^31,
+ * outside [0, T*tk) is skipped.  No output overlaps an input.  Requires 1 <= tk <= 32, T*tk < 2^31,
  * I % 8 == 0 (I % 32 == 0 with y_scales); y (8-byte with y_scales), dh, dy and
  * hw 16-byte aligned.  No workspace. */
 int moe_swiglu_backward(const void* y, const uint8_t* y_scales, const void* dh,

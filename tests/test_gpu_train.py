@@ -565,6 +565,19 @@ def test_block_training_step(dev, T, H, E, tk, I, ckpt):
     assert torch.equal(a1, 2 * g["dw_first"]) and torch.equal(a2, 2 * g["dw_down"])
 
 
+def test_training_step_without_tokens(dev):
+    say("train step T=0")
+    rng = np.random.default_rng(1)
+    _, w1, w2, _, _ = block(rng, 1, 128, 2, 1, 128)
+    q1, q2 = pipeline.prepare_weights(dev_vals(w1)), pipeline.prepare_weights(dev_vals(w2))
+    x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    out, st = pipeline.moe_train_forward(x, torch.empty((0, 2), device="cuda"), 1, q1, q2)
+    g = pipeline.moe_train_backward(st, x)
+    torch.cuda.synchronize()
+    assert out.shape == g["dx"].shape == (0, 128) and g["d_topk_w"].shape == (0, 1)
+    assert not g["dw_first"].any() and not g["dw_down"].any()
+
+
 def test_training_step_graph_replays_match_eager(dev):
     """Forward and backward captured as one graph; every replay, with eager
     calls between, gives the eager bits, also for new inputs in place."""
