@@ -125,7 +125,8 @@ __device__ __forceinline__ void wait_and_barrier() {
 // Input gradient, one 32x64 block of a wave: sc * acc to columns k0 .. + 63 of
 // rows r0 .. r0 + 31 of a matrix of `rows` rows of K at `out` (bf16, or the
 // float32 part of a slice), through 4 KB of the wave's own LDS in 128-byte
-// rows.
+// rows.  bf16 rows are stored nontemporally (131072 rows of 1536: 1.51 ->
+// 1.50 ms); the parts of slices are read again at once.
 template <typename T>
 __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2], float sc, T* out,
                                           int64_t rows, uint32_t r0, uint32_t k0, uint32_t K) {
@@ -160,7 +161,7 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
       const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 128 + ((lc ^ (r & 7)) << 4));
       const uint32_t k = k0 + 32 * h + lc * (16 / sizeof(T));
       __builtin_amdgcn_raw_buffer_store_b128(
-          v, rs, k < K ? ((r0 + r) * K + k) * (uint32_t)sizeof(T) : kPastBuffer, 0, 0);
+          v, rs, k < K ? ((r0 + r) * K + k) * (uint32_t)sizeof(T) : kPastBuffer, 0, kF32 ? 0 : 2);
     }
   }
 }
@@ -175,8 +176,10 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // k_dgrad_join adds them.
 //
 // A row tile of an expert's last 128 (64) rows or fewer is multiplied with 64
-// (32) rows per wave: it costs its weights' decode, not a full tile's products
-// (2048 rows over 128 experts 275 -> 207 us).  Measured: 131072 rows,
+// (32) rows per wave and loads only the 128 (64) rows of dy that those read: it
+// costs its weights' decode, not a full tile's products (2048 rows over 128
+// experts 275 -> 207 us; 64 rows for each of 128 experts of 1536x2048, without
+// the loads of rows that are not there, 124 -> 98 us).  Measured: 131072 rows,
 // 128 experts of 4096x1536, 1.53 ms = 1.08 PFLOP/s; 32768 rows, 128 experts of
 // 1536x2048 (half the experts a tile and a tail), 0.28 ms.  Without the weight
 // decode the first took 1.30 instead of 1.59 ms; matrix units 53% busy, at
@@ -277,11 +280,16 @@ k_dgrad(GradArgs p, int n_tiles) {
     wscales[set] = __builtin_amdgcn_raw_buffer_load_b16(
         rs_s, there ? off_ws : kPastBuffer, there ? (uint32_t)u * (w_step >> 3) : 0, 0);
   };
-  auto issue_a = [&](uint8_t* st, int u) __attribute__((always_inline)) {
+  using c0 = std::integral_constant<int, 0>;
+  using c1 = std::integral_constant<int, 1>;
+  using c2 = std::integral_constant<int, 2>;
+  using c4 = std::integral_constant<int, 4>;
+  // (the first 64 NV rows of a stage: a tail's waves read no others)
+  auto issue_a = [&](uint8_t* st, int u, auto nv_c) __attribute__((always_inline)) {
     const bool there = u < u1 && (uint32_t)u * BC + 8 * a_c < (uint32_t)p.N;
     const uint32_t so = u < u1 ? (uint32_t)u * (2 * BC) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < decltype(nv_c)::value; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(st + (i * 8 + wave) * 1024), 16,
                                                there ? off_a[i] : kPastBuffer, so, 0, 0);
   };
@@ -297,13 +305,13 @@ k_dgrad(GradArgs p, int n_tiles) {
   const TrLane tr(lane);
   const int a_sw = (r32 >> 1) & 7;
   issue_w(0, u0);
-  issue_a(sa0, u0);
+  issue_a(sa0, u0, c4{});
   issue_w(1, u0 + 1);
-  issue_a(sa1, u0 + 1);
+  issue_a(sa1, u0 + 1, c4{});
 #pragma unroll
   for (int j = 0; j < 4; ++j) fill(sb0, 0, j);
   issue_w(0, u0 + 2);
-  issue_a(sa2, u0 + 2);
+  issue_a(sa2, u0 + 2, c4{});
   wait_and_barrier<12>();
   // the tile with NV 32-row blocks per row of waves; whole, so that no
   // accumulator is merged between variants
@@ -353,16 +361,13 @@ k_dgrad(GradArgs p, int n_tiles) {
       read(sa[AU], sb[BU], 3);
       fill(sb[BU ^ 1], BU ^ 1, 3);
       multiply(2);
-      wait_and_barrier<6>();
+      wait_and_barrier<2 + NV>();
       issue_w(BU ^ 1, u + 3);
-      issue_a(sa[AU], u + 3);
+      issue_a(sa[AU], u + 3, nv_c);
       read(sa[(AU + 1) % 3], sb[BU ^ 1], 0);
       multiply(3);
     };
     read(sa0, sb0, 0);
-    using c0 = std::integral_constant<int, 0>;
-    using c1 = std::integral_constant<int, 1>;
-    using c2 = std::integral_constant<int, 2>;
     for (int u = u0; u < u1;) {
       step(c0{}, c0{}, u);
       if (++u >= u1) break;
@@ -392,9 +397,9 @@ k_dgrad(GradArgs p, int n_tiles) {
                   (uint32_t)p.K);
     }
   };
-  if (hi - a0 > 128) whole(std::integral_constant<int, 4>{});
-  else if (hi - a0 > 64) whole(std::integral_constant<int, 2>{});
-  else whole(std::integral_constant<int, 1>{});
+  if (hi - a0 > 128) whole(c4{});
+  else if (hi - a0 > 64) whole(c2{});
+  else whole(c1{});
 }
 
 // ---------------------------------------------------------------------------
