@@ -93,11 +93,6 @@ k_tile_prefix(const int32_t* __restrict__ offsets, int E, int64_t M_total, int b
   if (tid == E - 1) prefix[E] = base + incl;
 }
 
-void tile_prefix(const int32_t* offsets, int E, int64_t M_total, int bm, int32_t* prefix,
-                 hipStream_t s) {
-  k_tile_prefix<<<1, 1024, 0, s>>>(offsets, E, M_total, bm, prefix);
-}
-
 __global__ void __launch_bounds__(256)
 k_gemm_generic(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smA[kBM * kRowBytes];

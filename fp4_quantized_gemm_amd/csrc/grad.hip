@@ -22,7 +22,7 @@ struct GradArgs {
   const uint8_t* w_scales;
   const float* g_w;
   const int32_t* offsets;      // [E + 1]
-  const int32_t* prefix;       // dgrad: row tiles before each expert
+  const int32_t* prefix;       // dgrad: whole tiles and tails before each expert
   uint16_t* dx;                // dgrad: [M_total][K] bf16
   void* dw;                    // wgrad: [E][N][K] f32 or bf16
   int64_t M_dy, M_x, M_total, N, K;
@@ -175,22 +175,61 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // contraction is split: each slice writes its float32 part (times g_w), and
 // k_dgrad_join adds them.
 //
-// A row tile of an expert's last 128 (64) rows or fewer is multiplied with 64
-// (32) rows per wave and loads only the 128 (64) rows of dy that those read: it
+// An expert's last 128 rows or fewer are a tail, multiplied with 64 (32 if at
+// most 64) rows per wave and loading only the rows of dy that those read: it
 // costs its weights' decode, not a full tile's products (2048 rows over 128
 // experts 275 -> 207 us; 64 rows for each of 128 experts of 1536x2048, without
-// the loads of rows that are not there, 124 -> 98 us).  Measured: 131072 rows,
-// 128 experts of 4096x1536, 1.53 ms = 1.08 PFLOP/s; 32768 rows, 128 experts of
-// 1536x2048 (half the experts a tile and a tail), 0.28 ms.  Without the weight
-// decode the first took 1.30 instead of 1.59 ms; matrix units 53% busy, at
-// 1.8 GHz: the chip's power limit, then LDS and vector instructions beside the
-// products.  A persistent form (one workgroup per CU) was slower, 1.57 ms and
-// 0.31 ms.
+// the loads of rows that are not there, 124 -> 98 us).  Tails follow all whole
+// tiles, so that every XCD has its share of both and the cheaper ones end the
+// launch; an expert's weights are then read a second time, which costs less
+// (32768 skewed rows 0.280 -> 0.261 ms, 16384 rows over 128 experts of
+// 4096x1536 0.357 -> 0.308 ms).
+//
+// Measured: 131072 rows, 128 experts of 4096x1536, 1.42 ms = 1.16 PFLOP/s;
+// 32768 rows, 128 experts of 1536x2048 (half the experts a tile and a tail),
+// 0.26 ms.  When the first took 1.59 ms it took 1.30 without the weight decode,
+// and the matrix units were 53% busy at 1.8 GHz: the chip's power limit, then
+// LDS and vector instructions beside the products.  A persistent form (one
+// workgroup per CU) was slower, 1.57 against 1.53 ms and 0.31 against 0.28.
 // ---------------------------------------------------------------------------
 namespace dg {
 constexpr int BC = 64;
 constexpr int A_BYTES = kTile * BC * 2, B_BYTES = BC * kTile * 2;   // 32768 each
 }  // namespace dg
+
+// An expert's rows are whole tiles and, where 1 to 128 rows are left, a tail:
+// prefix[e], prefix[E + 1 + e] = whole tiles and tails of the experts before e.
+constexpr int kTail = 128;
+
+__global__ void __launch_bounds__(1024)
+k_dgrad_tiles(GradArgs p, int32_t* __restrict__ prefix) {
+  __shared__ uint64_t wsum[16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  uint64_t v = 0;   // whole tiles below, tails above
+  if (tid < p.E) {
+    int64_t lo, hi;
+    expert_rows(p, tid, lo, hi);
+    const int64_t left = (hi - lo) % kTile;
+    v = (uint64_t)((hi - lo) / kTile + (left > kTail)) |
+        (uint64_t)(left > 0 && left <= kTail) << 32;
+  }
+  uint64_t incl = v;
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t u = __shfl_up(incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 63) wsum[tid >> 6] = incl;
+  __syncthreads();
+  for (int w = 0; w < (tid >> 6); ++w) incl += wsum[w];
+  if (tid >= p.E) return;
+  const uint64_t before = incl - v;
+  prefix[tid] = (int32_t)before;
+  prefix[p.E + 1 + tid] = (int32_t)(before >> 32);
+  if (tid == p.E - 1) {
+    prefix[p.E] = (int32_t)incl;
+    prefix[2 * p.E + 1] = (int32_t)(incl >> 32);
+  }
+}
 
 __global__ void __launch_bounds__(512, 1)
 k_dgrad(GradArgs p, int n_tiles) {
@@ -211,31 +250,37 @@ k_dgrad(GradArgs p, int n_tiles) {
   uint8_t* const sa[3] = {sa0, sa1, sa2};
   uint8_t* const sb[2] = {sb0, sb1};
 
-  // tile: groups of 4 row tiles x all column tiles, a contiguous range of
-  // that order per XCD (workgroup b runs on XCD b % 8, each with its own L2)
+  // tile: whole row tiles first, then tails; of each, groups of 4 row tiles x
+  // all column tiles, a contiguous range of that order per XCD (workgroup b
+  // runs on XCD b % 8, each with its own L2)
   int e, nt;
   int64_t lo, hi, a0;
   {
-    const int b = (int)blockIdx.x;
-    const int real_m = p.prefix[p.E];
-    const int real_blocks = ((real_m + 3) / 4) * 4 * n_tiles;
-    const int per_xcd = (real_blocks + 7) / 8;
-    if ((b >> 3) >= per_xcd) return;
-    const int v = (b & 7) * per_xcd + (b >> 3);
-    if (v >= real_blocks) return;
+    const int n_whole = p.prefix[p.E], n_tail = p.prefix[2 * p.E + 1];
     const int group = 4 * n_tiles;
+    const int per_whole = ((n_whole + 3) / 4 * group + 7) / 8;
+    const int per_tail = ((n_tail + 3) / 4 * group + 7) / 8;
+    const int xcd = (int)blockIdx.x & 7;
+    int i = (int)blockIdx.x >> 3;
+    const bool tail = i >= per_whole;
+    if (tail) i -= per_whole;
+    if (i >= (tail ? per_tail : per_whole)) return;
+    const int32_t* const prefix = p.prefix + (tail ? p.E + 1 : 0);
+    const int real_m = tail ? n_tail : n_whole;
+    const int v = xcd * (tail ? per_tail : per_whole) + i;
     const int gi = v / group, g = v - gi * group;
     const int gm = real_m - 4 * gi < 4 ? real_m - 4 * gi : 4;
+    if (gm <= 0) return;
     const int gt = 4 * gi + g % gm;
     nt = g / gm;
-    if (gt >= real_m || nt >= n_tiles) return;
+    if (nt >= n_tiles) return;
     // the last expert whose first tile is at or before gt: 64 at a time
     int n = 0;
-    for (int i = 0; i < p.E; i += 64)
-      n += __builtin_popcountll(__ballot(i + lane < p.E && p.prefix[i + lane] <= gt));
+    for (int j = 0; j < p.E; j += 64)
+      n += __builtin_popcountll(__ballot(j + lane < p.E && prefix[j + lane] <= gt));
     e = __builtin_amdgcn_readfirstlane(n - 1);
     expert_rows(p, e, lo, hi);
-    a0 = lo + (int64_t)(gt - p.prefix[e]) * kTile;
+    a0 = lo + (tail ? (hi - lo) / kTile : gt - prefix[e]) * kTile;
   }
   const int64_t b0 = (int64_t)nt * kTile;
   // this slice's steps (all of them without a split)
@@ -1069,7 +1114,7 @@ using namespace nvfp4;
 
 extern "C" {
 
-static size_t dgrad_prefix_bytes(int64_t E) { return round_up((size_t)(E + 1) * sizeof(int32_t), 256); }
+static size_t dgrad_prefix_bytes(int64_t E) { return round_up(2 * (size_t)(E + 1) * sizeof(int32_t), 256); }
 
 size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
   if (E < 1 || M_total < 0 || N < 1 || K < 1) return 256;
@@ -1131,10 +1176,11 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   } else {
     const int64_t n_tiles = (K + kTile - 1) / kTile;
     const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
-    const int64_t blocks = ((m_tiles + 3) / 4 * 4 * n_tiles + 7) / 8 * 8;
+    // (whole tiles and tails are each rounded up to groups of 4 and to 8 XCDs)
+    const int64_t blocks = ((m_tiles + 6) * n_tiles + 7) / 8 * 8 + 16;
     NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
                "grouped_w4a16_dgrad: more than 2^22 tiles");
-    tile_prefix(expert_offsets, (int)E, M_total, kTile, static_cast<int32_t*>(ws), s);
+    k_dgrad_tiles<<<1, 1024, 0, s>>>(p, static_cast<int32_t*>(ws));
     k_dgrad<<<dim3((unsigned)blocks, (unsigned)p.nsplit), 512, 0, s>>>(p, (int)n_tiles);
   }
   if (p.nsplit > 1) {

@@ -24,9 +24,4 @@ constexpr int kBufferRsrcWord3 = 0x00020000;
 typedef __attribute__((address_space(3))) void* lds_void_ptr;
 __device__ __forceinline__ lds_void_ptr lds_ptr(void* p) { return (lds_void_ptr)p; }
 
-// prefix[e] = number of bm-row tiles of the experts before e, prefix[E] = of
-// all of them (one workgroup; E <= 1024); defined in gemm.hip
-void tile_prefix(const int32_t* offsets, int E, int64_t M_total, int bm, int32_t* prefix,
-                 hipStream_t s);
-
 }  // namespace nvfp4

@@ -419,7 +419,7 @@ int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * [M_total][K] bf16; rows outside [off[0], off[E]) are left as they were.
  * The weights are the packed copy the forward takes.  Same rules for the
  * expert grouping as grouped_w4a16_gemm; dx overlaps no input.  The workspace
- * holds a tile prefix and, where the tiles fill less than the chip, float32
+ * holds tile prefixes and, where the tiles fill less than the chip, float32
  * parts of up to 16 slices of n, summed in a fixed order.  Requires
  * 1 <= E <= 1024, M_total < 2^31, N % 16 == 0, K % 64 == 0, N and K <= 2^20,
  * M_src * N * 2 < 2^32, N * K / 2 < 2^32; dy_rows == NULL needs

@@ -192,6 +192,22 @@ def test_dgrad(dev, counts, N, K, gather):
     check_dgrad(host_vals(dx), ref, mag, N, "dx")
 
 
+@pytest.mark.parametrize("counts,K", [
+    ([128, 129, 0, 256, 257, 384, 385, 64, 65], 320),     # every kind of last tile
+    ([256, 512, 256], 1088),                              # no tails
+    ([100, 0, 64, 128, 1, 127], 576),                     # nothing but tails
+    ([2, 640, 3] + [40] * 70, 64),                        # tails past the first 64 experts
+])
+def test_dgrad_row_tile_edges(dev, counts, K):
+    say(f"dgrad edges {counts} K={K}")
+    rng = np.random.default_rng(sum(counts) + K)
+    dy, rows, wc, ws, gw, offs = dgrad_case(rng, counts, 80, K, True)
+    dx = run_dgrad(dy, rows, wc, ws, gw, offs, M_total=int(offs[-1]))
+    torch.cuda.synchronize()
+    ref, mag = OT.grouped_dgrad(dy, rows, wc, ws, gw, offs)
+    check_dgrad(host_vals(dx), ref, mag, 80, "dx")
+
+
 def test_dgrad_is_the_forward_transposed(dev):
     """<dy, W x> = <W^T dy, x> with the forward's own product."""
     say("dgrad adjoint")
