@@ -1044,12 +1044,13 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // fills past the end
 }
 
-// The input gradient's few-row kernel: up to 32 rows per expert on average
-// (128 experts of 4096x1536: 210 us at 32 rows on either, 110 against 298 at
-// 8, 281 against 214 at 48), or 64 rows in all (one expert, 64 rows of
-// 4096x1536: 21.6 against 22.9 us, 100 rows 33 against 24).
+// The input gradient's few-row kernel: up to 16 rows per expert on average,
+// routed at random (128 experts of 1536x2048: 68 against 87 us at 16 rows, 97
+// against 92 at 24, 119 against 101 at 32; 8 of 4096x4096: 35 against 34 at
+// 16, 43 against 34 at 24), or 64 rows in all (one expert of 4096x1536, 64
+// rows: 15 against 18 us, 100 rows 31 against 22).
 static bool dgrad_few_rows(int64_t E, int64_t M_total) {
-  return M_total <= 32 * E || M_total <= 64;
+  return M_total <= 16 * E || M_total <= 64;
 }
 
 // Slices of n, at most 16, each of eight steps of 64 or more: for the few-row
@@ -1062,8 +1063,11 @@ static int dgrad_split(int64_t E, int64_t M_total, int64_t N, int64_t K) {
   if (dgrad_few_rows(E, M_total)) {
     s = 4096 / ((E < M_total ? E : (M_total < 1 ? 1 : M_total)) * (K / 64));
   } else {
-    // (an expert's last tile is half full on average)
-    s = 256 / (((M_total + kTile - 1) / kTile + E / 2) * ((K + kTile - 1) / kTile));
+    // (an expert's last tile is half full on average, and every expert has one:
+    // 256 rows over 8 experts of 4096x4096, 45 us with three slices, 35 with two)
+    int64_t tiles = (M_total + kTile - 1) / kTile + E / 2;
+    tiles = tiles < E ? E : tiles;
+    s = 256 / (tiles * ((K + kTile - 1) / kTile));
   }
   s = s > steps / 8 ? steps / 8 : s;
   s = s < 1 ? 1 : (s > 16 ? 16 : s);
