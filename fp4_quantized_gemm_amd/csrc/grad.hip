@@ -116,10 +116,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint6
 }
 
 template <int N>
-__device__ __forceinline__ void wait_and_barrier() {
+__device__ __forceinline__ void wait_for() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N < 63 ? N : 63) : "memory");
+}
+
+__device__ __forceinline__ void barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  wait_for<N>();
+  barrier();
 }
 
 // Input gradient, one 32x64 block of a wave: sc * acc to columns k0 .. + 63 of
@@ -688,7 +697,7 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   __shared__ __attribute__((aligned(16))) uint8_t st3[STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t outb[8 * OUT];
   constexpr int kOps = (MX ? 6 : 4) + (LA ? 2 : 0) + (LB ? 2 : 0);
-  constexpr int kStores = 16;   // bf16; float32 has 32, and waits for half of them
+  constexpr int kStores = 16;   // of a bf16 tile; a float32 one has twice as many
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -1023,8 +1032,10 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     read(stage[j], 1);
     multiply(0);
     const WgStep next = next_step(j % 2 == 0);
-    if (behind < 3) wait_and_barrier<2 * kOps + kStores>();
-    else wait_and_barrier<2 * kOps>();
+    if (behind >= 3) wait_for<2 * kOps>();
+    else if (p.dw_bf16) wait_for<2 * kOps + kStores>();
+    else wait_for<2 * kOps + 2 * kStores>();
+    barrier();
     ++behind;
     read(stage[j1], 0);
     issue(stage[j], j);
