@@ -934,22 +934,38 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
     // rows n0 + 8 q + lr, 16-byte chunk lc of the 128-byte piece at column k0
     auto rows_out = [&](const __amdgpu_buffer_rsrc_t& rs_o, uint32_t n0, uint32_t k0,
                         uint32_t bytes) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      auto at = [&](int q) __attribute__((always_inline)) {
+        const uint32_t n = n0 + 8 * q + lr, k = k0 + lc * (16 / bytes);
+        return n < N && k < K ? (n * K + k) * bytes : kPastBuffer;
+      };
+      auto mine = [&](int q) __attribute__((always_inline)) {
         const int r = 8 * q + lr;
-        u32x4 v = *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
-        const uint32_t n = n0 + r, k = k0 + lc * (16 / bytes);
-        const uint32_t o = n < N && k < K ? (n * K + k) * bytes : kPastBuffer;
-        if (bytes == 4 && p.accumulate) {
-          const auto old = __builtin_amdgcn_raw_buffer_load_b128(rs_o, o, 0, 0);
+        return *reinterpret_cast<const u32x4*>(ob + r * 128 + ((lc ^ (r & 7)) << 4));
+      };
+      // nontemporal stores: dw is not read back soon, and its lines leave L2 to
+      // the operands (wgrad of 32768 rows, 128 experts of 1536x2048: 0.52 ->
+      // 0.37 ms)
+      if (bytes == 4 && p.accumulate) {
+        // all four loads before the first store, which none of them would be
+        // moved across: 0.83 -> 0.65 ms there (a block further ahead spills)
+        u32x4 was[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const auto w = __builtin_amdgcn_raw_buffer_load_b128(rs_o, at(q), 0, 0);
+          was[q] = u32x4{w[0], w[1], w[2], w[3]};
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u32x4 v = mine(q);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(old[c]));
+            v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(was[q][c]));
+          __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, at(q), 0, 2);
         }
-        // nontemporal: dw is not read back soon, and its lines leave L2 to the
-        // operands (wgrad of 32768 rows, 128 experts of 1536x2048: 0.52 ->
-        // 0.37 ms)
-        __builtin_amdgcn_raw_buffer_store_b128(v, rs_o, o, 0, 2);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          __builtin_amdgcn_raw_buffer_store_b128(mine(q), rs_o, at(q), 0, 2);
       }
     };
     if (p.dw_bf16) {
