@@ -194,7 +194,7 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // (32768 skewed rows 0.280 -> 0.261 ms, 16384 rows over 128 experts of
 // 4096x1536 0.357 -> 0.308 ms).
 //
-// Measured: 131072 rows, 128 experts of 4096x1536, 1.42 ms = 1.16 PFLOP/s;
+// Measured: 131072 rows, 128 experts of 4096x1536, 1.42 to 1.47 ms = 1.15 PFLOP/s;
 // 32768 rows, 128 experts of 1536x2048 (half the experts a tile and a tail),
 // 0.26 ms.  When the first took 1.59 ms it took 1.30 without the weight decode,
 // and the matrix units were 53% busy at 1.8 GHz: the chip's power limit, then
