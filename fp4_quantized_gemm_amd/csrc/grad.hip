@@ -188,7 +188,8 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // most 64) rows per wave and loading only the rows of dy that those read: it
 // costs its weights' decode, not a full tile's products (2048 rows over 128
 // experts 275 -> 207 us; 64 rows for each of 128 experts of 1536x2048, without
-// the loads of rows that are not there, 124 -> 98 us).  Tails follow all whole
+// the loads of rows that are not there, 124 -> 98 us); 129 to 192 rows likewise
+// take 96 per wave (160 rows each: 169 -> 147 us).  Tails follow all whole
 // tiles, so that every XCD has its share of both and the cheaper ones end the
 // launch; an expert's weights are then read a second time, which costs less
 // (32768 skewed rows 0.280 -> 0.261 ms, 16384 rows over 128 experts of
@@ -196,7 +197,7 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 //
 // Measured: 131072 rows, 128 experts of 4096x1536, 1.42 to 1.47 ms = 1.15 PFLOP/s;
 // 32768 rows, 128 experts of 1536x2048 (half the experts a tile and a tail),
-// 0.26 ms.  When the first took 1.59 ms it took 1.30 without the weight decode,
+// 0.25 ms.  When the first took 1.59 ms it took 1.30 without the weight decode,
 // and the matrix units were 53% busy at 1.8 GHz: the chip's power limit, then
 // LDS and vector instructions beside the products.  A persistent form (one
 // workgroup per CU) was slower, 1.57 against 1.53 ms and 0.31 against 0.28.
@@ -332,8 +333,9 @@ k_dgrad(GradArgs p, int n_tiles) {
   using c0 = std::integral_constant<int, 0>;
   using c1 = std::integral_constant<int, 1>;
   using c2 = std::integral_constant<int, 2>;
+  using c3 = std::integral_constant<int, 3>;
   using c4 = std::integral_constant<int, 4>;
-  // (the first 64 NV rows of a stage: a tail's waves read no others)
+  // (the first 64 NV rows of a stage: the waves read no others)
   auto issue_a = [&](uint8_t* st, int u, auto nv_c) __attribute__((always_inline)) {
     const bool there = u < u1 && (uint32_t)u * BC + 8 * a_c < (uint32_t)p.N;
     const uint32_t so = u < u1 ? (uint32_t)u * (2 * BC) : 0;
@@ -446,9 +448,11 @@ k_dgrad(GradArgs p, int n_tiles) {
                   (uint32_t)p.K);
     }
   };
-  if (hi - a0 > 128) whole(c4{});
-  else if (hi - a0 > 64) whole(c2{});
-  else whole(c1{});
+  const int nv = hi - a0 > 192 ? 4 : (int)(hi - a0 + 63) / 64;
+  if (nv == 4) { whole(c4{}); return; }
+  if (nv == 3) { whole(c3{}); return; }
+  if (nv == 2) { whole(c2{}); return; }
+  whole(c1{});
 }
 
 // ---------------------------------------------------------------------------

@@ -195,6 +195,7 @@ def test_dgrad(dev, counts, N, K, gather):
 @pytest.mark.parametrize("counts,K", [
     ([128, 129, 0, 256, 257, 384, 385, 64, 65], 320),     # every kind of last tile
     ([256, 512, 256], 1088),                              # no tails
+    ([191, 192, 193, 448, 449, 130], 256),                # whole tiles of three and four parts
     ([100, 0, 64, 128, 1, 127], 576),                     # nothing but tails
     ([2, 640, 3] + [40] * 70, 64),                        # tails past the first 64 experts
 ])
