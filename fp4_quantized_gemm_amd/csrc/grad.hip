@@ -465,7 +465,7 @@ k_dgrad(GradArgs p, int n_tiles) {
 // of the expert per pass; more re-stream the weights.
 //
 // Measured: 2048 rows over 128 experts of 4096x1536, 115 us = 4.0 TB/s of
-// weights (207 us tile by tile); one row of one such expert 20 us.  Bound by
+// weights (161 us tile by tile); one row of one such expert 20 us.  Bound by
 // its vector instructions (two per decoded weight, 16 per 8) and their issue,
 // with three waves per SIMD; with up to 64 rows per pass and two waves per SIMD
 // 146 us.
