@@ -1070,6 +1070,17 @@ k_wgrad(GradArgs p, int n_tiles, int m_tiles) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // fills past the end
 }
 
+// Sizes that a call takes.  Its workspace query asks the same first: the
+// splits below divide by tile counts, which other sizes make zero or overflow.
+static bool dgrad_sizes(int64_t E, int64_t M_total, int64_t N, int64_t K) {
+  return E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 31) && N >= 16 && N % 16 == 0 &&
+         N <= (1LL << 20) && K >= 64 && K % 64 == 0 && K <= (1LL << 20);
+}
+static bool wgrad_sizes(int64_t E, int64_t M_total, int64_t N, int64_t K) {
+  return E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 30) && N >= 8 && N % 8 == 0 &&
+         N <= (1LL << 20) && K >= 8 && K % 8 == 0 && K <= (1LL << 20);
+}
+
 // The input gradient's few-row kernel: up to 16 rows per expert on average,
 // routed at random (128 experts of 1536x2048: 68 against 87 us at 16 rows, 97
 // against 92 at 24, 119 against 101 at 32; 8 of 4096x4096: 35 against 34 at
@@ -1147,7 +1158,7 @@ extern "C" {
 static size_t dgrad_prefix_bytes(int64_t E) { return round_up(2 * (size_t)(E + 1) * sizeof(int32_t), 256); }
 
 size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 256;
+  if (!dgrad_sizes(E, M_total, N, K)) return 256;   // the call refuses them
   const int sp = dgrad_split(E, M_total, N, K);
   return dgrad_prefix_bytes(E) +
          (sp > 1 ? round_up((size_t)sp * (size_t)M_total * (size_t)K * 4, 256) : 0);
@@ -1157,10 +1168,7 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
                         const uint8_t* w_codes, const uint8_t* w_scales, const float* g_w,
                         const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N,
                         int64_t K, void* dx, void* ws, size_t ws_bytes, void* stream) {
-  NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 31) && M_src >= 0 &&
-                 N >= 16 && N % 16 == 0 && K >= 64 && K % 64 == 0 && N <= (1LL << 20) &&
-                 K <= (1LL << 20),
-             NVFP4_ERR_SHAPE,
+  NV_REQUIRE(dgrad_sizes(E, M_total, N, K) && M_src >= 0, NVFP4_ERR_SHAPE,
              "grouped_w4a16_dgrad: need 1 <= E <= 1024, M_total < 2^31, N %% 16 == 0, K %% 64 == 0, "
              "N and K up to 2^20 (E=%lld M_total=%lld N=%lld K=%lld)",
              (long long)E, (long long)M_total, (long long)N, (long long)K);
@@ -1225,7 +1233,7 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
 }
 
 size_t grouped_wgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 256;
+  if (!wgrad_sizes(E, M_total, N, K)) return 256;   // the call refuses them
   const int sp = wgrad_split(E, M_total, N, K);
   return sp > 1 ? round_up((size_t)sp * (size_t)E * (size_t)N * (size_t)K * 4, 256) : 256;
 }
@@ -1234,9 +1242,8 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
                   const uint8_t* x_scales, const int32_t* x_rows, int64_t M_x,
                   const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
                   void* dw, int dw_bf16, int accumulate, void* ws, size_t ws_bytes, void* stream) {
-  NV_REQUIRE(E >= 1 && E <= 1024 && M_total >= 0 && M_total < (1LL << 30) && M_dy >= 0 &&
-                 M_x >= 0 && N >= 8 && N % 8 == 0 && K >= 8 && K % 8 == 0 && N <= (1LL << 20) &&
-                 K <= (1LL << 20) && (x_scales == nullptr || K % 32 == 0),
+  NV_REQUIRE(wgrad_sizes(E, M_total, N, K) && M_dy >= 0 && M_x >= 0 &&
+                 (x_scales == nullptr || K % 32 == 0),
              NVFP4_ERR_SHAPE,
              "grouped_wgrad: need 1 <= E <= 1024, M_total < 2^30, N %% 8 == 0, K %% 8 == 0 "
              "(K %% 32 == 0 for 8-bit x), N and K up to 2^20 (E=%lld M_total=%lld N=%lld K=%lld)",

@@ -1,6 +1,9 @@
 """Refusals of the training-step calls, on the CPU: every call below fails its
 argument checks before it touches memory or launches anything."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -119,3 +122,38 @@ def test_binding_refuses_host_tensors():
         F.moe_swiglu_backward(b, b)
     with pytest.raises(F.NvfpError, match="device tensor"):
         F.grouped_w4a16_dgrad(b, None, b, b, b, i)
+
+
+SIZES = [-(1 << 63), -1, 0, 1, 8, 16, 32, 63, 64, 65, 96, 1024, 1025, (1 << 20), (1 << 20) + 64, 1 << 22,
+         1 << 24, 1 << 30, 1 << 31, 1 << 40, 1 << 62, (1 << 63) - 1]
+
+
+@pytest.mark.parametrize("query", ["grouped_w4a16_dgrad_workspace_size",
+                                   "grouped_wgrad_workspace_size"])
+def test_workspace_queries_survive_every_size(query):
+    """A caller asks before the call that would refuse its sizes.  (In a process
+    of its own: a division by zero there ends it.)"""
+    code = ("import itertools, sys, fp4_quantized_gemm_amd as F\n"
+            f"q = F.lib().{query}\n"
+            "for a in itertools.product(%r, repeat=4):\n"
+            "    n = q(*a)\n"
+            "    assert 256 <= n < 1 << 62, (a, n)\n" % (SIZES,))
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+
+
+@pytest.mark.parametrize("E,M,N,K", [(1, 1, 16, 32), (1, 1, 24, 64), (1, 1, 16, 96), (1025, 8, 16, 64),
+                                     (1, 1 << 31, 16, 64), (1, 1, (1 << 20) + 16, 64),
+                                     (1, 1, 16, (1 << 20) + 64)])
+def test_dgrad_query_of_refused_sizes(E, M, N, K):
+    assert F.lib().grouped_w4a16_dgrad_workspace_size(E, M, N, K) == 256
+    assert dgrad(E=E, P=M, N=N, K=K) == ERR_SHAPE
+
+
+@pytest.mark.parametrize("E,M,N,K", [(1, 1, 4, 64), (1, 1, 64, 12), (1025, 8, 16, 64),
+                                     (1, 1 << 30, 16, 64), (1, 1, (1 << 20) + 8, 64),
+                                     (1, 1, 16, (1 << 20) + 8)])
+def test_wgrad_query_of_refused_sizes(E, M, N, K):
+    assert F.lib().grouped_wgrad_workspace_size(E, M, N, K) == 256
+    assert wgrad(E=E, P=M, N=N, K=K) == ERR_SHAPE
