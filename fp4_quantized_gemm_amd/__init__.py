@@ -613,6 +613,14 @@ def mxfp8_restore(codes, scales, out=None):
     return out
 
 
+def _whole_blocks(scales, cols, name):
+    """An 8-bit operand has whole blocks of 32 columns.  (The scales of fewer
+    than 32 have no elements and so no address, and without one the library
+    reads the operand as bf16.)"""
+    if scales is not None and (cols < 32 or cols % 32):
+        raise NvfpError(f"8-bit {name} must have a multiple of 32 columns, got {cols}")
+
+
 def _m_total(M_total, default, *row_lists):
     """Rows of the permuted side: as given, else a row list's length, else
     the default."""
@@ -669,6 +677,7 @@ def grouped_wgrad(dy, dy_rows, x, x_rows, expert_offsets, x_scales=None, M_total
     xp = _arg(x, torch.bfloat16 if x_scales is None else torch.uint8, "x", dev, (None, None))
     (M_dy, N), (M_x, K) = dy.shape, x.shape
     sp = _arg(x_scales, torch.uint8, "x_scales", dev, (M_x, K // 32), optional=True)
+    _whole_blocks(x_scales, K, "x")
     drp = _arg(dy_rows, torch.int32, "dy_rows", dev, (None,), optional=True)
     xrp = _arg(x_rows, torch.int32, "x_rows", dev, (None,), optional=True)
     op = _arg(expert_offsets, torch.int32, "expert_offsets", dev, (None,))
@@ -706,6 +715,7 @@ def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h
     if I2 != 2 * I:
         raise NvfpError("y must be [gate | up]")
     sp = _arg(y_scales, torch.uint8, "y_scales", dev, (P, I2 // 32), optional=True)
+    _whole_blocks(y_scales, I, "gate and up")
     dhp = _arg(dh, torch.bfloat16, "dh", dev, (P, I))
     ip = _arg(inv_perm, torch.int32, "inv_perm", dev, (None, None), optional=True)
     T, tk = (P, 1) if inv_perm is None else inv_perm.shape

@@ -157,3 +157,48 @@ def test_dgrad_query_of_refused_sizes(E, M, N, K):
 def test_wgrad_query_of_refused_sizes(E, M, N, K):
     assert F.lib().grouped_wgrad_workspace_size(E, M, N, K) == 256
     assert wgrad(E=E, P=M, N=N, K=K) == ERR_SHAPE
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on the device, for what the binding
+    checks before it calls the library."""
+    is_cuda = True
+
+
+def there(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library calls the binding makes, recorded instead of made."""
+    made = []
+    monkeypatch.setattr(F, "_call", lambda name, dev, *a: made.append((name, a)))
+    return made
+
+
+@pytest.mark.parametrize("K", [8, 16, 24, 40])
+def test_binding_refuses_8_bit_x_of_part_blocks(calls, K):
+    """Under 32 columns the scales have no elements, hence no address: the
+    library would take the codes for bf16 values and read past their end."""
+    with pytest.raises(F.NvfpError, match="32"):
+        F.grouped_wgrad(there(4, 64), None, there(4, K, dtype=torch.uint8), None,
+                        there(2, dtype=torch.int32), x_scales=there(4, K // 32, dtype=torch.uint8))
+    assert not calls
+
+
+@pytest.mark.parametrize("I", [8, 24, 40])
+def test_binding_refuses_8_bit_y_of_part_blocks(calls, I):
+    with pytest.raises(F.NvfpError, match="32"):
+        F.moe_swiglu_backward(there(4, 2 * I, dtype=torch.uint8), there(4, I),
+                              y_scales=there(4, 2 * I // 32, dtype=torch.uint8))
+    assert not calls
+
+
+def test_binding_passes_8_bit_operands_on(calls):
+    u8 = torch.uint8
+    F.grouped_wgrad(there(4, 64), None, there(4, 32, dtype=u8), None, there(2, dtype=torch.int32),
+                    x_scales=there(4, 1, dtype=u8))
+    F.moe_swiglu_backward(there(4, 64, dtype=u8), there(4, 32), y_scales=there(4, 2, dtype=u8))
+    assert [c[0] for c in calls] == ["grouped_wgrad", "moe_swiglu_backward"]
+    assert calls[0][1][4] and calls[1][1][1]                         # the scales' addresses
