@@ -75,8 +75,10 @@ __device__ __forceinline__ int64_t source_row(const int32_t* rows, int64_t p, in
 constexpr int kTile = 256;
 
 // an offset past every buffer: such a load returns zeros, such a store is
-// dropped
+// dropped.  (Rows are a multiple of 16 bytes, so a buffer below 4 GiB ends
+// there at the latest.)
 constexpr uint32_t kPastBuffer = 0xFFFFFFF0u;
+constexpr uint64_t kMaxBytes = (1ULL << 32) - 1;
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4_t* lds_tr_ptr;
@@ -1175,7 +1177,7 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   NV_REQUIRE(dy_rows != nullptr || M_src >= M_total, NVFP4_ERR_SHAPE,
              "grouped_w4a16_dgrad: without dy_rows, M_src must be >= M_total");
   NV_REQUIRE(M_total == 0 || M_src >= 1, NVFP4_ERR_SHAPE, "grouped_w4a16_dgrad: M_src == 0");
-  NV_REQUIRE((uint64_t)M_src < (1ULL << 32) / (2 * (uint64_t)N) &&
+  NV_REQUIRE((uint64_t)M_src <= kMaxBytes / (2 * (uint64_t)N) &&
                  (uint64_t)N * (uint64_t)K / 2 < (1ULL << 32),
              NVFP4_ERR_UNSUPPORTED, "grouped_w4a16_dgrad: dy or one expert's codes exceed 4 GiB");
   NV_REQUIRE(w_codes && w_scales && g_w && expert_offsets && ws && (M_total == 0 || (dy && dx)),
@@ -1252,8 +1254,8 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
              NVFP4_ERR_SHAPE, "grouped_wgrad: an operand without a row list needs M_total rows");
   NV_REQUIRE(M_total == 0 || (M_dy >= 1 && M_x >= 1), NVFP4_ERR_SHAPE,
              "grouped_wgrad: an operand has no rows");
-  NV_REQUIRE((uint64_t)M_dy < (1ULL << 32) / (2 * (uint64_t)N) &&
-                 (uint64_t)M_x < (1ULL << 32) / ((x_scales ? 1 : 2) * (uint64_t)K),
+  NV_REQUIRE((uint64_t)M_dy <= kMaxBytes / (2 * (uint64_t)N) &&
+                 (uint64_t)M_x <= kMaxBytes / ((x_scales ? 1 : 2) * (uint64_t)K),
              NVFP4_ERR_UNSUPPORTED, "grouped_wgrad: dy or x exceeds 4 GiB");
   NV_REQUIRE((uint64_t)N * (uint64_t)K < (1ULL << 30), NVFP4_ERR_UNSUPPORTED,
              "grouped_wgrad: one expert's dw has 2^30 elements or more");

@@ -202,3 +202,26 @@ def test_binding_passes_8_bit_operands_on(calls):
     F.moe_swiglu_backward(there(4, 64, dtype=u8), there(4, 32), y_scales=there(4, 2, dtype=u8))
     assert [c[0] for c in calls] == ["grouped_wgrad", "moe_swiglu_backward"]
     assert calls[0][1][4] and calls[1][1][1]                         # the scales' addresses
+
+
+@pytest.mark.parametrize("N,last", [(48, 44739242), (80, 26843545), (16, (1 << 27) - 1)])
+def test_dgrad_takes_dy_up_to_its_stated_limit(N, last):
+    """M_src * N * 2 < 2^32, exactly: a workspace of 4 bytes stops the call
+    after the check of sizes."""
+    assert last * N * 2 < 1 << 32 <= (last + 1) * N * 2
+    assert dgrad(M=last, N=N, wb=4) == ERR_WS
+    assert dgrad(M=last + 1, N=N, wb=4) == ERR_UNSUP
+    assert dgrad(M=(1 << 63) - 1, N=N, wb=4) == ERR_UNSUP
+
+
+@pytest.mark.parametrize("C,xs,last", [(24, None, 89478485), (8, None, (1 << 28) - 1), (96, A, 44739242),
+                                       (32, A, (1 << 27) - 1)])
+def test_wgrad_takes_operands_up_to_their_stated_limit(C, xs, last):
+    size = 1 if xs else 2
+    assert last * C * size < 1 << 32 <= (last + 1) * C * size
+    assert wgrad(xr=A, Mx=last, K=C, xs=xs, wb=4) == ERR_WS
+    assert wgrad(xr=A, Mx=last + 1, K=C, xs=xs, wb=4) == ERR_UNSUP
+    if not xs:
+        assert wgrad(dyr=A, Md=last, N=C, wb=4) == ERR_WS
+        assert wgrad(dyr=A, Md=last + 1, N=C, wb=4) == ERR_UNSUP
+        assert wgrad(dyr=A, Md=(1 << 63) - 1, N=C, wb=4) == ERR_UNSUP

@@ -701,3 +701,47 @@ def test_binding_refusals(dev):
         F.moe_swiglu_backward(b, b[:, :32].contiguous(), rows[:2].view(1, 2))
     with pytest.raises(F.NvfpError, match="shape"):
         F.moe_swiglu_backward(b, b)
+
+
+def test_gradients_of_operands_of_the_last_size(dev):
+    """The largest dy and x below 4 GiB whose rows do not divide it: the last
+    row gathered, rows and columns past an edge still read as zeros."""
+    rng = np.random.default_rng(31)
+    n = 40
+    offs = cu(np.array([0, 13, 13, 40], np.int32))
+
+    def far_rows(M):
+        rows = torch.from_numpy(np.sort(rng.choice(M, n, replace=False))).cuda()
+        rows[-1], rows[0] = M - 1, 0
+        order = torch.from_numpy(rng.permutation(n)).cuda()
+        return rows, rows[order].int(), order.int()
+
+    N, M = 48, 44739242                                  # 64 bytes below
+    say(f"dgrad dy of {M * N * 2} bytes")
+    rows, far, near = far_rows(M)
+    small = dev_vals(heavy_bf16(rng, (n, N)))
+    big = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    big[rows] = small
+    w = F.nvfp4_qdq_weights(dev_vals(OF.round_to_bf16(rng.standard_normal((3, N, 192)) * 0.02)),
+                            want_qdq=False)
+    W = (w.packed_codes, w.packed_scales, w.g)
+    for extra in (0, 60):                                # both kernels, by the rows allowed for
+        f, m = (torch.cat([t, t[:1].expand(extra)]) for t in (far, near))
+        a = F.grouped_w4a16_dgrad(big, f, *W, offs)
+        b = F.grouped_w4a16_dgrad(small, m, *W, offs)
+        assert torch.equal(a[:n].view(torch.int16), b[:n].view(torch.int16))
+        assert bool(torch.isfinite(a[:n].float()).all())
+    del big
+
+    C, M = 24, 89478485                                  # 16 bytes below
+    say(f"wgrad operand of {M * C * 2} bytes")
+    rows, far, near = far_rows(M)
+    small = dev_vals(heavy_bf16(rng, (n, C)))
+    big = torch.full((M, C), float("nan"), dtype=torch.bfloat16, device="cuda")
+    big[rows] = small
+    other = dev_vals(heavy_bf16(rng, (n, 64)))
+    for args, ref in [((big, far, other, None), (small, near, other, None)),
+                      ((other, None, big, far), (other, None, small, near))]:
+        a, b = F.grouped_wgrad(*args, offs), F.grouped_wgrad(*ref, offs)
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+        assert bool(torch.isfinite(a).all())
