@@ -1207,9 +1207,7 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + dgrad_prefix_bytes(E));
   if (dgrad_few_rows(E, M_total)) {
     const int64_t groups = (K + 255) / 256;
-    const int64_t blocks = E * groups * p.nsplit;
-    NV_REQUIRE(blocks < (1LL << 23), NVFP4_ERR_UNSUPPORTED,
-               "grouped_w4a16_dgrad: more than 2^23 tiles");
+    const int64_t blocks = E * groups * p.nsplit;   // 2^22 at most, by the sizes and the split
     // (33 to 64 rows in all: the two passes an expert may need side by side)
     k_dgrad_few<<<dim3((unsigned)blocks, M_total > 32 && M_total <= 64 ? 2 : 1), 256, 0, s>>>(
         p, (int)groups);
@@ -1218,8 +1216,8 @@ int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
     const int64_t m_tiles = (M_total + kTile - 1) / kTile + E;   // the most there can be
     // (whole tiles and tails are each rounded up to 8 XCDs)
     const int64_t blocks = (m_tiles * n_tiles + 14) / 8 * 8;
-    NV_REQUIRE(blocks < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
-               "grouped_w4a16_dgrad: more than 2^22 tiles");
+    NV_REQUIRE(m_tiles * n_tiles + 14 < (1LL << 22), NVFP4_ERR_UNSUPPORTED,
+               "grouped_w4a16_dgrad: 2^22 tiles of 256x256 or more");
     k_dgrad_tiles<<<1, 1024, 0, s>>>(p, static_cast<int32_t*>(ws));
     k_dgrad<<<dim3((unsigned)blocks, (unsigned)p.nsplit), 512, 0, s>>>(p, (int)n_tiles);
   }

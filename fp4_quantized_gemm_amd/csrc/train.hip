@@ -207,8 +207,8 @@ int mxfp8_checkpoint(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* 
   NV_REQUIRE(M >= 0 && K >= 32 && K % 32 == 0 && ldx >= K && ldx % 8 == 0 &&
                  M < (1LL << 40) && K < (1LL << 22),
              NVFP4_ERR_SHAPE,
-             "mxfp8_checkpoint: need M >= 0, K %% 32 == 0, ldx >= K, ldx %% 8 == 0 "
-             "(M=%lld K=%lld ldx=%lld)",
+             "mxfp8_checkpoint: need 0 <= M < 2^40, K %% 32 == 0, 32 <= K < 2^22, ldx >= K, "
+             "ldx %% 8 == 0 (M=%lld K=%lld ldx=%lld)",
              (long long)M, (long long)K, (long long)ldx);
   NV_REQUIRE(h == nullptr || K % 64 == 0, NVFP4_ERR_SHAPE,
              "mxfp8_checkpoint: the SwiGLU needs K %% 64 == 0 (K=%lld)", (long long)K);
@@ -240,8 +240,8 @@ int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
   NV_REQUIRE(M >= 0 && K >= 32 && K % 32 == 0 && ldx >= K && ldx % 8 == 0 &&
                  M < (1LL << 40) && K < (1LL << 22),
              NVFP4_ERR_SHAPE,
-             "mxfp8_restore: need M >= 0, K %% 32 == 0, ldx >= K, ldx %% 8 == 0 "
-             "(M=%lld K=%lld ldx=%lld)",
+             "mxfp8_restore: need 0 <= M < 2^40, K %% 32 == 0, 32 <= K < 2^22, ldx >= K, "
+             "ldx %% 8 == 0 (M=%lld K=%lld ldx=%lld)",
              (long long)M, (long long)K, (long long)ldx);
   if (M == 0) return ok();
   NV_REQUIRE(codes && scales && x, NVFP4_ERR_NULL, "mxfp8_restore: missing pointer");
@@ -263,8 +263,8 @@ int moe_swiglu_backward(const void* y, const uint8_t* y_scales, const void* dh,
   NV_REQUIRE(T >= 0 && tk >= 1 && tk <= 32 && T < (1LL << 31) && T * tk < (1LL << 31) && I >= 8 &&
                  I % 8 == 0 && I < (1LL << 31) && (y_scales == nullptr || I % 32 == 0),
              NVFP4_ERR_SHAPE,
-             "moe_swiglu_backward: need T >= 0, 1 <= tk <= 32, T*tk < 2^31, I %% 8 == 0 "
-             "(I %% 32 == 0 for 8-bit y) (T=%lld tk=%lld I=%lld)",
+             "moe_swiglu_backward: need T >= 0, 1 <= tk <= 32, T*tk < 2^31, 8 <= I < 2^31, "
+             "I %% 8 == 0 (I %% 32 == 0 for 8-bit y) (T=%lld tk=%lld I=%lld)",
              (long long)T, (long long)tk, (long long)I);
   if (T == 0) return ok();
   NV_REQUIRE(y && dh && dy, NVFP4_ERR_NULL, "moe_swiglu_backward: missing pointer");

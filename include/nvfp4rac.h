@@ -402,10 +402,12 @@ int grouped_fp8_gemm(const uint8_t* a, const float* g_x, const int32_t* a_rows, 
  *   codes and scales (both or neither NULL).  h [M][K/2] bf16 or NULL: with
  *   x = [gate | up], h = bf16(silu(gate) * up) from the same read (the same
  *   bits as nvfp4_quantize_act with glu = 1); codes NULL: h alone.
- *   Requires M >= 0, K % 32 == 0 (K % 64 == 0 with h), ldx % 8 == 0;
- *   codes 8-byte, scales unaligned, x and h 16-byte aligned.  No workspace.
+ *   Requires 0 <= M < 2^40, K % 32 == 0 (K % 64 == 0 with h), 32 <= K < 2^22,
+ *   ldx >= K, ldx % 8 == 0; codes 8-byte, scales unaligned, x and h 16-byte
+ *   aligned.  No workspace.
  * mxfp8_restore: x [M][K] bf16 (row stride ldx) = code * scale, exactly, for
- *   codes and scales that mxfp8_checkpoint wrote.  No workspace.
+ *   codes and scales that mxfp8_checkpoint wrote.  Same limits and alignment.
+ *   No workspace.
  * ---------------------------------------------------------------------- */
 int mxfp8_checkpoint(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
                      uint8_t* scales, void* h, void* stream);
@@ -423,7 +425,9 @@ int mxfp8_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * parts of up to 16 slices of n, summed in a fixed order.  Requires
  * 1 <= E <= 1024, M_total < 2^31, N % 16 == 0, K % 64 == 0, N and K <= 2^20,
  * M_src * N * 2 < 2^32, N * K / 2 < 2^32; dy_rows == NULL needs
- * M_src >= M_total. */
+ * M_src >= M_total.  With more than 16 E rows (and more than 64), the row
+ * tiles of 256 times the column tiles of 256 are fewer than 2^22:
+ * (ceil(M_total / 256) + E) * ceil(K / 256) + 14 < 2^22. */
 size_t grouped_w4a16_dgrad_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_w4a16_dgrad(const void* dy, const int32_t* dy_rows, int64_t M_src,
                         const uint8_t* w_codes, const uint8_t* w_scales, const float* g_w,
@@ -463,9 +467,11 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
  *   d_topk_w[t][j] = sum_i dh_i gate_i s_i up_i   float32 [T][tk] or NULL
  * The gradient of the routing logits follows from d_topk_w as that of a
  * softmax over the tk chosen experts.  inv_perm is a permutation; an entry
- * outside [0, T*tk) is skipped.  No output overlaps an input.  Requires 1 <= tk <= 32, T*tk < 2^31,
- * I % 8 == 0 (I % 32 == 0 with y_scales); y (8-byte with y_scales), dh, dy and
- * hw 16-byte aligned.  No workspace. */
+ * outside [0, T*tk) is skipped: its d_topk_w, and the rows that no entry
+ * names, are left as they were.  No output overlaps an input.  Requires
+ * 1 <= tk <= 32, T*tk < 2^31, I % 8 == 0 (I % 32 == 0 with y_scales),
+ * 8 <= I < 2^31; y (8-byte with y_scales), dh, dy and hw 16-byte aligned.  No
+ * workspace. */
 int moe_swiglu_backward(const void* y, const uint8_t* y_scales, const void* dh,
                         const int32_t* inv_perm, const float* topk_w, int64_t T, int64_t tk,
                         int64_t I, void* dy, void* hw, float* d_topk_w, void* stream);

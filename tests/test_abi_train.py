@@ -225,3 +225,22 @@ def test_wgrad_takes_operands_up_to_their_stated_limit(C, xs, last):
         assert wgrad(dyr=A, Md=last, N=C, wb=4) == ERR_WS
         assert wgrad(dyr=A, Md=last + 1, N=C, wb=4) == ERR_UNSUP
         assert wgrad(dyr=A, Md=(1 << 63) - 1, N=C, wb=4) == ERR_UNSUP
+
+
+def test_stated_limits():
+    """Sizes refused for a limit that the header and the message name."""
+    L = F.lib()
+
+    def said():
+        return L.nvfp4_last_error().decode()
+    # row tiles of 256 rows times column tiles of 256
+    assert dgrad(E=1, P=1 << 30, N=16, K=64) == ERR_UNSUP and "2^22" in said()
+    assert dgrad(E=1, P=(1 << 30) - 256 * 15, N=16, K=64) == ERR_UNSUP and "2^22" in said()
+    assert dgrad(E=1024, P=1 << 20, N=16, K=1 << 20) == ERR_UNSUP and "2^22" in said()
+    assert L.mxfp8_checkpoint(A, 1, 1 << 22, 1 << 22, A, A, None, None) == ERR_SHAPE
+    assert "2^22" in said()
+    assert L.mxfp8_restore(A, A, 1, 1 << 22, A, 1 << 22, None) == ERR_SHAPE and "2^22" in said()
+    assert L.mxfp8_checkpoint(A, 1 << 40, 64, 64, A, A, None, None) == ERR_SHAPE
+    assert "2^40" in said()
+    assert L.mxfp8_restore(A, A, 1 << 40, 64, A, 64, None) == ERR_SHAPE and "2^40" in said()
+    assert swiglu(T=1, tk=1, I=1 << 31) == ERR_SHAPE and "I < 2^31" in said()
