@@ -18,7 +18,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
+from . import (NvfpError, _arg, _wshape, grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
                grouped_w4a4_gemm_rac_per_expert, grouped_w4a4_gemm_rac_swiglu, grouped_wgrad,
                moe_permute, moe_swiglu_backward, mxfp8_checkpoint, nvfp4_quantize_act_amax,
                moe_unpermute_combine, nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act,
@@ -158,15 +158,24 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     the weight gradients are added to (gradient accumulation).  The routing
     weight enters in the SwiGLU's backward pass, so d_out goes into both of the
     down projection's products as it is, gathered by token."""
+    # all that the weight gradients could refuse, before one of them has been
+    # added to (their own limits are the stricter for the first product's,
+    # which has twice the columns: it comes first)
     acc1, acc2 = dw_first is not None, dw_down is not None
+    for name, out, w in (("dw_first", dw_first, st.w_first), ("dw_down", dw_down, st.w_down)):
+        E, N = _wshape(w.packed_codes)
+        _arg(out, torch.float32, name, d_out.device, (E, N, w.packed_codes.shape[3] * 64),
+             optional=True)
+    if not (acc1 and acc2) and dw_dtype not in (torch.float32, torch.bfloat16):
+        raise NvfpError(f"dw_dtype must be float32 or bfloat16, not {dw_dtype}")
     rows = st.perm_token.numel()
     dh = grouped_w4a16_dgrad(d_out, st.perm_token, st.w_down.packed_codes, st.w_down.packed_scales,
                              st.w_down.g, st.offsets, M_total=rows)
     dy1, hw, d_tw = moe_swiglu_backward(st.y1, dh, st.inv_perm, st.topk_w, y_scales=st.y1_scales)
-    g_down = grouped_wgrad(d_out, st.perm_token, hw, None, st.offsets, M_total=rows,
-                           dtype=dw_dtype, out=dw_down, accumulate=acc2)
     g_first = grouped_wgrad(dy1, None, st.x, st.perm_token, st.offsets, x_scales=st.x_scales,
                             M_total=rows, dtype=dw_dtype, out=dw_first, accumulate=acc1)
+    g_down = grouped_wgrad(d_out, st.perm_token, hw, None, st.offsets, M_total=rows,
+                           dtype=dw_dtype, out=dw_down, accumulate=acc2)
     dxp = grouped_w4a16_dgrad(dy1, None, st.w_first.packed_codes, st.w_first.packed_scales,
                               st.w_first.g, st.offsets, M_total=rows)
     dx = moe_unpermute_combine(dxp, st.inv_perm, torch.ones_like(st.topk_w))

@@ -1,0 +1,97 @@
+"""Arguments of pipeline.moe_train_forward and moe_train_backward, on the CPU:
+what does not fit together is refused before any call is made, so a refused
+backward pass has added nothing to the gradients it was given.  The library's
+calls are recorded instead of made."""
+import pytest
+import torch
+
+import fp4_quantized_gemm_amd as F
+from fp4_quantized_gemm_amd import pipeline
+from tests.test_abi_train import there
+
+T, H, E, TK, I = 6, 384, 4, 2, 128
+F32, BF16, I32, U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+
+
+def weights(e, n, k):
+    return pipeline.QuantWeights(None, None, there(e, dtype=F32), None,
+                                 there(e, 2, n // 16, k // 64, 16, 32, dtype=U8),
+                                 there(e, 2, n // 16, k // 64, 16, 4, dtype=U8))
+
+
+def state(**kw):
+    P = T * TK
+    s = dict(x=there(T, H, dtype=U8), x_scales=there(T, H // 32, dtype=U8),
+             y1=there(P, 2 * I, dtype=U8), y1_scales=there(P, 2 * I // 32, dtype=U8),
+             topk_ids=there(T, TK, dtype=I32), topk_w=there(T, TK, dtype=F32),
+             offsets=there(E + 1, dtype=I32), perm_token=there(P, dtype=I32),
+             inv_perm=there(T, TK, dtype=I32), w_first=weights(E, 2 * I, H),
+             w_down=weights(E, H, I))
+    return pipeline.TrainState(**{**s, **kw})
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """(name, keyword arguments) of every call, none made."""
+    made = []
+    P = T * TK
+
+    def stub(name, result):
+        def call(*a, **kw):
+            made.append((name, kw))
+            return result(*a, **kw) if callable(result) else result
+        monkeypatch.setattr(pipeline, name, call)
+
+    stub("moe_permute", (there(T, TK, dtype=I32), there(T, TK, dtype=F32), there(E + 1, dtype=I32),
+                         there(P, dtype=I32), there(T, TK, dtype=I32)))
+    stub("grouped_w4a16_gemm", there(P, 2 * I))
+    stub("mxfp8_checkpoint", dict(codes=there(P, 2 * I, dtype=U8),
+                                  scales=there(P, 2 * I // 32, dtype=U8), h=there(P, I)))
+    stub("moe_unpermute_combine", there(T, H))
+    stub("grouped_w4a16_dgrad", there(P, I))
+    stub("moe_swiglu_backward", (there(P, 2 * I), there(P, I), there(T, TK, dtype=F32)))
+    stub("grouped_wgrad", lambda *a, **kw: kw.get("out"))
+    return made
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dw_first=there(E, 2 * I, H)),                               # bf16 cannot be added to
+    dict(dw_first=there(E, H, 2 * I, dtype=F32)),
+    dict(dw_first=there(E, 2 * I, 2 * H, dtype=F32)[:, :, ::2]),
+    dict(dw_first=torch.zeros(E, 2 * I, H)),                         # a host tensor
+    dict(dw_first=there(E, 2 * I, H, dtype=F32), dw_down=there(E, I, H, dtype=F32)),
+    dict(dw_dtype=torch.float16),                                    # of dw_first, which is not given
+])
+def test_a_refused_backward_has_added_nothing(calls, kw):
+    kw.setdefault("dw_down", there(E, H, I, dtype=F32))
+    with pytest.raises(F.NvfpError):
+        pipeline.moe_train_backward(state(), there(T, H), **kw)
+    assert not calls
+
+
+def test_the_larger_weight_gradient_comes_first(calls, monkeypatch):
+    """Limits that only grouped_wgrad knows (4 GiB operands, 2^30 elements of
+    dw) are passed by the down projection's whenever they are by the first's."""
+    first = there(E, 2 * I, H, dtype=F32)
+
+    def refuse(*a, **kw):
+        if kw["out"] is first:
+            raise F.NvfpError("dy or x exceeds 4 GiB")
+        calls.append(("grouped_wgrad", kw))
+    monkeypatch.setattr(pipeline, "grouped_wgrad", refuse)
+    with pytest.raises(F.NvfpError, match="4 GiB"):
+        pipeline.moe_train_backward(state(), there(T, H), dw_first=first,
+                                    dw_down=there(E, H, I, dtype=F32))
+    assert "grouped_wgrad" not in [c[0] for c in calls]
+
+
+def test_backward_runs(calls):
+    first, down = there(E, 2 * I, H, dtype=F32), there(E, H, I, dtype=F32)
+    g = pipeline.moe_train_backward(state(), there(T, H), dw_first=first, dw_down=down,
+                                    dw_dtype=None)
+    assert g["dw_first"] is first and g["dw_down"] is down
+    assert all(c[1]["accumulate"] for c in calls if c[0] == "grouped_wgrad")
+    for dt in (F32, BF16):
+        del calls[:]
+        pipeline.moe_train_backward(state(), there(T, H), dw_dtype=dt)
+        assert [c[1]["dtype"] for c in calls if c[0] == "grouped_wgrad"] == [dt, dt]
