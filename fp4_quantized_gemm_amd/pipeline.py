@@ -158,6 +158,9 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     the weight gradients are added to (gradient accumulation).  The routing
     weight enters in the SwiGLU's backward pass, so d_out goes into both of the
     down projection's products as it is, gathered by token."""
+    # (d_out is gathered by token, a token past its end as its last row)
+    T, H = st.topk_w.shape[0], _wshape(st.w_down.packed_codes)[1]
+    _arg(d_out, torch.bfloat16, "d_out", st.topk_w.device, (T, H))
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
     # which has twice the columns: it comes first)

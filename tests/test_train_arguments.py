@@ -85,6 +85,14 @@ def test_the_larger_weight_gradient_comes_first(calls, monkeypatch):
     assert "grouped_wgrad" not in [c[0] for c in calls]
 
 
+@pytest.mark.parametrize("d_out", [there(T - 1, H), there(T + 1, H), there(T * H), there(T, 2 * H)])
+def test_backward_refuses_d_out_of_other_tokens(calls, d_out):
+    """Its rows are gathered by token: too few would be read as the last one."""
+    with pytest.raises(F.NvfpError, match="d_out"):
+        pipeline.moe_train_backward(state(), d_out)
+    assert not calls
+
+
 def test_backward_runs(calls):
     first, down = there(E, 2 * I, H, dtype=F32), there(E, H, I, dtype=F32)
     g = pipeline.moe_train_backward(state(), there(T, H), dw_first=first, dw_down=down,
