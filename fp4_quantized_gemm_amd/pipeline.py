@@ -125,6 +125,25 @@ class TrainState:
     w_down: QuantWeights
 
 
+def _check_block(x, logits, bias, w_first, w_down):
+    """The operands of a block fit together: the products take their sizes
+    from one operand and index the others with them on the device."""
+    dev = getattr(x, "device", None)
+    _arg(x, torch.bfloat16, "x", dev, (None, None))
+    T, H = x.shape
+    _arg(logits, torch.float32, "logits", dev, (T, None))
+    E = logits.shape[1]
+    _arg(bias, torch.float32, "bias", dev, optional=True)
+    if bias is not None and bias.numel() != E:
+        raise NvfpError(f"bias must have {E} elements, got {bias.numel()}")
+    n = _wshape(w_first.packed_codes)[1]
+    for name, w, N, K in (("w_first", w_first, n, H), ("w_down", w_down, H, n // 2)):
+        tiles = (E, 2, N // 16, K // 64, 16)
+        _arg(w.packed_codes, torch.uint8, f"{name}'s codes", dev, tiles + (32,))
+        _arg(w.packed_scales, torch.uint8, f"{name}'s scales", dev, tiles + (4,))
+        _arg(w.g, torch.float32, f"{name}'s tensor scales", dev, (E,))
+
+
 def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, bias=None,
                       checkpoint="mxfp8"):
     """The block with the trainer's W4A16 products (bf16 activations): x [T][H]
@@ -134,6 +153,7 @@ def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeigh
     them as they are."""
     if checkpoint not in ("mxfp8", "bf16"):
         raise ValueError(f"checkpoint must be 'mxfp8' or 'bf16', not {checkpoint!r}")
+    _check_block(x, logits, bias, w_first, w_down)
     mx = checkpoint == "mxfp8"
     ids, tw, offs, perm, inv = moe_permute(logits, topk, bias)
     rows = perm.numel()

@@ -103,3 +103,36 @@ def test_backward_runs(calls):
         del calls[:]
         pipeline.moe_train_backward(state(), there(T, H), dw_dtype=dt)
         assert [c[1]["dtype"] for c in calls if c[0] == "grouped_wgrad"] == [dt, dt]
+
+
+def forward(x=None, logits=None, topk=TK, w_first=None, w_down=None, **kw):
+    return pipeline.moe_train_forward(
+        there(T, H) if x is None else x, there(T, E, dtype=F32) if logits is None else logits, topk,
+        w_first or weights(E, 2 * I, H), w_down or weights(E, H, I), **kw)
+
+
+@pytest.mark.parametrize("kw,name", [
+    (dict(x=there(T - 1, H)), "logits"), (dict(x=there(T + 1, H)), "logits"),
+    (dict(x=torch.zeros(T, H, dtype=BF16)), "x"), (dict(x=there(T, H, dtype=F32)), "x"),
+    (dict(logits=there(T, E - 1, dtype=F32)), "w_first"),            # offsets of E - 1 experts
+    (dict(logits=there(T, E + 1, dtype=F32)), "w_first"),
+    (dict(x=there(T, 2 * H)), "w_first"),                            # weights read past their end
+    (dict(w_first=weights(E + 1, 2 * I, H)), "w_first"),
+    (dict(w_down=weights(E + 1, H, I)), "w_down"), (dict(w_down=weights(E, H, 2 * I)), "w_down"),
+    (dict(w_down=weights(E, 2 * H, I)), "w_down"), (dict(w_first=weights(E, I, H)), "w_down"),
+    (dict(bias=there(E - 1, dtype=F32)), "bias"), (dict(bias=there(E)), "bias"),
+    (dict(bias=torch.zeros(E)), "bias"),
+])
+def test_forward_refuses_what_does_not_fit(calls, kw, name):
+    """The products take their sizes from one operand and index the others
+    with them on the device."""
+    with pytest.raises(F.NvfpError, match=name):
+        forward(**kw)
+    assert not calls
+
+
+def test_forward_runs(calls):
+    out, st = forward(bias=there(E, dtype=F32))
+    assert out.shape == (T, H) and st.w_down.g.shape == (E,)
+    forward(bias=there(1, E, dtype=F32), checkpoint="bf16")
+    assert [c[0] for c in calls].count("grouped_w4a16_gemm") == 4
