@@ -14,6 +14,7 @@ and moe_train_backward returns the gradients.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -144,6 +145,12 @@ def _check_block(x, logits, bias, w_first, w_down):
         _arg(w.g, torch.float32, f"{name}'s tensor scales", dev, (E,))
 
 
+def _where(x):
+    """The calls of a step with x's device as the current one: those of the
+    rollout side launch on the current device."""
+    return torch.cuda.device(x.device) if x.device.type == "cuda" else nullcontext()
+
+
 def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, bias=None,
                       checkpoint="mxfp8"):
     """The block with the trainer's W4A16 products (bf16 activations): x [T][H]
@@ -154,7 +161,11 @@ def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeigh
     if checkpoint not in ("mxfp8", "bf16"):
         raise ValueError(f"checkpoint must be 'mxfp8' or 'bf16', not {checkpoint!r}")
     _check_block(x, logits, bias, w_first, w_down)
-    mx = checkpoint == "mxfp8"
+    with _where(x):
+        return _train_forward(x, logits, topk, w_first, w_down, bias, checkpoint == "mxfp8")
+
+
+def _train_forward(x, logits, topk, w_first, w_down, bias, mx):
     ids, tw, offs, perm, inv = moe_permute(logits, topk, bias)
     rows = perm.numel()
     y1 = grouped_w4a16_gemm(x, perm, w_first.packed_codes, w_first.packed_scales, w_first.g, offs,
@@ -184,13 +195,18 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
     # which has twice the columns: it comes first)
-    acc1, acc2 = dw_first is not None, dw_down is not None
     for name, out, w in (("dw_first", dw_first, st.w_first), ("dw_down", dw_down, st.w_down)):
         E, N = _wshape(w.packed_codes)
         _arg(out, torch.float32, name, d_out.device, (E, N, w.packed_codes.shape[3] * 64),
              optional=True)
-    if not (acc1 and acc2) and dw_dtype not in (torch.float32, torch.bfloat16):
+    if (dw_first is None or dw_down is None) and dw_dtype not in (torch.float32, torch.bfloat16):
         raise NvfpError(f"dw_dtype must be float32 or bfloat16, not {dw_dtype}")
+    with _where(d_out):
+        return _train_backward(st, d_out, dw_dtype, dw_first, dw_down)
+
+
+def _train_backward(st, d_out, dw_dtype, dw_first, dw_down):
+    acc1, acc2 = dw_first is not None, dw_down is not None
     rows = st.perm_token.numel()
     dh = grouped_w4a16_dgrad(d_out, st.perm_token, st.w_down.packed_codes, st.w_down.packed_scales,
                              st.w_down.g, st.offsets, M_total=rows)

@@ -7,7 +7,7 @@ import torch
 
 import fp4_quantized_gemm_amd as F
 from fp4_quantized_gemm_amd import pipeline
-from tests.test_abi_train import there
+from tests.test_abi_train import OnDevice, there
 
 T, H, E, TK, I = 6, 384, 4, 2, 128
 F32, BF16, I32, U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
@@ -136,3 +136,41 @@ def test_forward_runs(calls):
     assert out.shape == (T, H) and st.w_down.g.shape == (E,)
     forward(bias=there(1, E, dtype=F32), checkpoint="bf16")
     assert [c[0] for c in calls].count("grouped_w4a16_gemm") == 4
+
+
+@pytest.fixture
+def current(monkeypatch):
+    """Which device is current, as torch.cuda.device sets it."""
+    stack = ["cuda:0"]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = str(dev)
+
+        def __enter__(self):
+            stack.append(self.dev)
+
+        def __exit__(self, *exc):
+            stack.pop()
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(OnDevice, "device", property(lambda t: torch.device("cuda", 1)),
+                        raising=False)
+    return stack
+
+
+def test_a_step_runs_with_its_tensors_device_current(calls, current, monkeypatch):
+    """Some of the calls launch on the current device's default stream: all run
+    where the tensors are, and the device that was current is so again."""
+    where = []
+    for name in ["moe_permute", "grouped_w4a16_gemm", "mxfp8_checkpoint", "moe_unpermute_combine",
+                 "grouped_w4a16_dgrad", "moe_swiglu_backward", "grouped_wgrad"]:
+        def call(*a, _f=getattr(pipeline, name), **kw):
+            where.append(current[-1])
+            return _f(*a, **kw)
+        monkeypatch.setattr(pipeline, name, call)
+    forward()
+    pipeline.moe_train_backward(state(), there(T, H))
+    assert len(where) == 12 and set(where) == {"cuda:1"} and current == ["cuda:0"]
+    with pytest.raises(F.NvfpError):
+        forward(x=there(T - 1, H))
+    assert current == ["cuda:0"]
