@@ -745,3 +745,56 @@ def test_gradients_of_operands_of_the_last_size(dev):
         a, b = F.grouped_wgrad(*args, offs), F.grouped_wgrad(*ref, offs)
         assert torch.equal(a.view(torch.int32), b.view(torch.int32))
         assert bool(torch.isfinite(a).all())
+
+
+@pytest.mark.parametrize("ckpt", ["mxfp8", "bf16"])
+@pytest.mark.parametrize("T,H,E,tk,I", [(70, 256, 4, 2, 128), (3, 128, 8, 2, 128), (1, 128, 2, 1, 128),
+                                        (600, 256, 3, 1, 384), (150, 384, 40, 8, 256)])
+def test_block_backward_stage_by_stage(dev, T, H, E, tk, I, ckpt):
+    """Each call of moe_train_backward against the oracle on that call's own
+    GPU inputs, element by element; the step returns the bits of the calls made
+    one by one.  No token takes expert 1."""
+    say(f"stages T={T} H={H} E={E} tk={tk} I={I} {ckpt}")
+    rng = np.random.default_rng(T + H + E)
+    x, w1, w2, logits, d_out = block(rng, T, H, E, tk, I)
+    logits[:, 1] = -100.0
+    q1, q2 = pipeline.prepare_weights(dev_vals(w1)), pipeline.prepare_weights(dev_vals(w2))
+    _, st = pipeline.moe_train_forward(dev_vals(x), cu(logits), tk, q1, q2, checkpoint=ckpt)
+    dd = dev_vals(d_out)
+    W1, W2 = [(q.packed_codes, q.packed_scales, q.g) for q in (q1, q2)]
+    P, perm, o = T * tk, st.perm_token, st.offsets
+    dh = F.grouped_w4a16_dgrad(dd, perm, *W2, o, M_total=P)
+    dy1, hw, dtw = F.moe_swiglu_backward(st.y1, dh, st.inv_perm, st.topk_w, y_scales=st.y1_scales)
+    dw2 = F.grouped_wgrad(dd, perm, hw, None, o, M_total=P)
+    dw1 = F.grouped_wgrad(dy1, None, st.x, perm, o, x_scales=st.x_scales, M_total=P)
+    dxp = F.grouped_w4a16_dgrad(dy1, None, *W1, o, M_total=P)
+    g = pipeline.moe_train_backward(st, dd)
+    torch.cuda.synchronize()
+
+    offs, rows, inv = (t.cpu().numpy() for t in (o, perm, st.inv_perm))
+    w = st.topk_w.cpu().numpy()
+    assert offs[1] == offs[2] and offs[-1] == P
+    c1, s1, g1, _ = OQ.qdq_weights(w1)
+    c2, s2, g2, _ = OQ.qdq_weights(w2)
+    mx = ckpt == "mxfp8"
+    kx = host_vals(F.mxfp8_restore(st.x, st.x_scales) if mx else st.x)
+    ky = host_vals(F.mxfp8_restore(st.y1, st.y1_scales) if mx else st.y1)
+    dhv, dyv, hv, dxv = (host_vals(t) for t in (dh, dy1, hw, dxp))
+
+    check_dgrad(dhv, *OT.grouped_dgrad(d_out, rows, c2, s2, g2, offs), H, "dh")
+    ref = OT.swiglu_backward(ky, dhv, inv, w)
+    lims = swiglu_limits(ky, dhv, inv, w, ref)
+    for got, r, lim, what in zip((dyv, hv, dtw.cpu().numpy().astype(np.float64)), ref, lims,
+                                 ("dy1", "hw", "d_topk_w")):
+        check(got, r, lim, what)
+    n = int(np.diff(offs).max())
+    for got, (r, mag), what in ((dw2, OT.grouped_wgrad(d_out, rows, hv, None, offs), "dw_down"),
+                                (dw1, OT.grouped_wgrad(dyv, None, kx, rows, offs), "dw_first")):
+        check(got.cpu().numpy().astype(np.float64), r, n * U * mag + TINY, what)
+        assert not got[1].any()
+    check_dgrad(dxv, *OT.grouped_dgrad(dyv, None, c1, s1, g1, offs), 2 * I, "dxp")
+    terms = dxv[inv]
+    r = terms.sum(1)
+    check(host_vals(g["dx"]), r, np.abs(r) * 2.0 ** -8 + (tk + 1) * U * np.abs(terms).sum(1) + TINY, "dx")
+    for a, b in ((g["dw_down"], dw2), (g["dw_first"], dw1), (g["d_topk_w"], dtw)):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
