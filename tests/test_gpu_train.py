@@ -798,3 +798,83 @@ def test_block_backward_stage_by_stage(dev, T, H, E, tk, I, ckpt):
     check(host_vals(g["dx"]), r, np.abs(r) * 2.0 ** -8 + (tk + 1) * U * np.abs(terms).sum(1) + TINY, "dx")
     for a, b in ((g["dw_down"], dw2), (g["dw_first"], dw1), (g["d_topk_w"], dtw)):
         assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+def nvfp4_values(q):
+    """float64 weights [E][N][K], g included, of QdqWeights on the device."""
+    E, N, half = q.codes.shape
+    c = torch.stack([q.codes & 15, q.codes >> 4], 3).view(E, N, 2 * half).long()
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    v = torch.cat([grid, -grid])[c]
+    s = q.scales.view(torch.float8_e4m3fn).double()
+    return v * s.repeat_interleave(16, 2) * q.g.double()[:, None, None]
+
+
+@pytest.mark.parametrize("counts", [[2, 1], [37, 63]])
+@pytest.mark.parametrize("N,K", [(16, 1 << 20), (1 << 20, 64)])
+def test_dgrad_widest(dev, N, K, counts):
+    """N and K at their limit, on the few-row and the tiled kernel."""
+    say(f"dgrad widest N={N} K={K} {counts}")
+    gen = torch.Generator(device="cuda").manual_seed(N + counts[0])
+    q = F.nvfp4_qdq_weights(torch.randn(2, N, K, device="cuda", generator=gen).bfloat16() * 0.02,
+                            want_qdq=False)
+    offs = offsets_of(counts)
+    P = int(offs[-1])
+    dy = torch.randn(P, N, device="cuda", generator=gen).bfloat16()
+    dx = F.grouped_w4a16_dgrad(dy, None, q.packed_codes, q.packed_scales, q.g, cu(offs))
+    w = nvfp4_values(q)
+    for e in range(2):
+        d, got = dy[offs[e]:offs[e + 1]].double(), dx[offs[e]:offs[e + 1]].double()
+        ref, mag = d @ w[e], d.abs() @ w[e].abs()
+        assert bool(((got - ref).abs() <= ref.abs() * 2.0 ** -8 + (N + 2) * U * mag + TINY).all())
+
+
+@pytest.mark.parametrize("N,K", [(1 << 20, 8), (8, 1 << 20), (32768, 32760)])
+def test_wgrad_widest(dev, N, K):
+    """N and K at their limit, and a dw of 1 MiB less than 4 GiB."""
+    say(f"wgrad widest N={N} K={K}")
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    dy = torch.randn(5, N, device="cuda", generator=gen).bfloat16()
+    x = torch.randn(5, K, device="cuda", generator=gen).bfloat16()
+    offs = cu(np.array([0, 5], np.int32))
+    dw = F.grouped_wgrad(dy, None, x, None, offs)
+    db = F.grouped_wgrad(dy, None, x, None, offs, dtype=torch.bfloat16)
+    acc = F.grouped_wgrad(dy, None, x, None, offs, out=torch.ones_like(dw), accumulate=True)
+    for lo in range(0, N, 4096):                         # (float64 of all of it is 8 GiB)
+        d = dy[:, lo:lo + 4096].double().t().contiguous()
+        ref, lim = d @ x.double(), 5 * U * (d.abs() @ x.double().abs()) + TINY
+        got, gb, ga = (t[0, lo:lo + 4096].double() for t in (dw, db, acc))
+        assert bool(((got - ref).abs() <= lim).all())
+        assert bool(((gb - ref).abs() <= ref.abs() * 2.0 ** -8 + lim).all())
+        assert bool(((ga - ref - 1).abs() <= lim + U * ((ref + 1).abs() + lim)).all())
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_checkpoint_of_more_than_2_31_chunks(dev, glu):
+    """64-bit chunk numbers: a few rows among zeros get the codes they get by
+    themselves."""
+    K = 65536
+    M = ((1 << 35 if glu else 1 << 34) // K) + 3
+    torch.cuda.empty_cache()
+    need = M * K * 2 * 5 // 2 + (1 << 34)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of device memory")
+    say(f"checkpoint of {M} rows of {K}, glu={glu}")
+    rows = torch.tensor([0, 1, M // 2, M - 4, M - 3, M - 2, M - 1], device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    small = torch.randn(7, K, device="cuda", generator=gen).bfloat16()
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[rows] = small
+    a, b = F.mxfp8_checkpoint(x, glu=glu), F.mxfp8_checkpoint(small, glu=glu)
+
+    def written(t):
+        return int(t.view(torch.int64).ne(0).any(1).sum())
+    assert torch.equal(a["codes"][rows], b["codes"]) and written(a["codes"]) == 7
+    assert torch.equal(a["scales"][rows], b["scales"])
+    if glu:
+        assert torch.equal(a["h"][rows], b["h"]) and written(a["h"]) == 7
+    else:
+        F.mxfp8_restore(a["codes"], a["scales"], out=x.fill_(float("nan")))
+        assert torch.equal(x[rows], F.mxfp8_restore(b["codes"], b["scales"])) and written(x) == 7
+    del x, a, b
+    torch.cuda.empty_cache()
