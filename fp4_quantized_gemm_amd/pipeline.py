@@ -129,26 +129,39 @@ class TrainState:
 def _check_block(x, logits, bias, w_first, w_down):
     """The operands of a block fit together: the products take their sizes
     from one operand and index the others with them on the device."""
-    dev = getattr(x, "device", None)
-    _arg(x, torch.bfloat16, "x", dev, (None, None))
+    if not x.is_cuda or x.dtype is not torch.bfloat16 or x.dim() != 2:
+        _arg(x, torch.bfloat16, "x", x.device, (None, None))
     T, H = x.shape
-    _arg(logits, torch.float32, "logits", dev, (T, None))
-    E = logits.shape[1]
-    _arg(bias, torch.float32, "bias", dev, optional=True)
-    if bias is not None and bias.numel() != E:
-        raise NvfpError(f"bias must have {E} elements, got {bias.numel()}")
-    n = _wshape(w_first.packed_codes)[1]
+    if logits.dim() != 2 or logits.shape[0] != T:
+        raise NvfpError(f"logits must have shape [{T}, None], got {list(logits.shape)}")
+    dev, E = x.device, logits.shape[1]
+    if bias is not None:
+        _arg(bias, torch.float32, "bias", dev)
+        if bias.numel() != E:
+            raise NvfpError(f"bias must have {E} elements, got {bias.numel()}")
+    c = w_first.packed_codes
+    n = c.shape[2] * 16 if c.dim() == 6 else _wshape(c)[1]
     for name, w, N, K in (("w_first", w_first, n, H), ("w_down", w_down, H, n // 2)):
+        c, s, g = w.packed_codes, w.packed_scales, w.g
         tiles = (E, 2, N // 16, K // 64, 16)
-        _arg(w.packed_codes, torch.uint8, f"{name}'s codes", dev, tiles + (32,))
-        _arg(w.packed_scales, torch.uint8, f"{name}'s scales", dev, tiles + (4,))
-        _arg(w.g, torch.float32, f"{name}'s tensor scales", dev, (E,))
+        # one comparison for all of it; _arg names what is wrong
+        if c.shape != tiles + (32,) or s.shape != tiles + (4,) or g.shape != (E,) or \
+                not (c.device == s.device == g.device == dev):
+            _arg(c, torch.uint8, name + "'s codes", dev, tiles + (32,))
+            _arg(s, torch.uint8, name + "'s scales", dev, tiles + (4,))
+            _arg(g, torch.float32, name + "'s tensor scales", dev, (E,))
+
+
+_HERE = nullcontext()
 
 
 def _where(x):
     """The calls of a step with x's device as the current one: those of the
     rollout side launch on the current device."""
-    return torch.cuda.device(x.device) if x.device.type == "cuda" else nullcontext()
+    dev = x.device
+    if dev.type != "cuda" or dev.index == torch._C._cuda_getDevice():
+        return _HERE
+    return torch.cuda.device(dev)
 
 
 def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, bias=None,
@@ -190,15 +203,16 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     weight enters in the SwiGLU's backward pass, so d_out goes into both of the
     down projection's products as it is, gathered by token."""
     # (d_out is gathered by token, a token past its end as its last row)
-    T, H = st.topk_w.shape[0], _wshape(st.w_down.packed_codes)[1]
-    _arg(d_out, torch.bfloat16, "d_out", st.topk_w.device, (T, H))
+    T, H = st.topk_w.shape[0], st.w_down.packed_codes.shape[2] * 16
+    if d_out.shape != (T, H):
+        raise NvfpError(f"d_out must have shape {[T, H]}, got {list(d_out.shape)}")
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
     # which has twice the columns: it comes first)
     for name, out, w in (("dw_first", dw_first, st.w_first), ("dw_down", dw_down, st.w_down)):
-        E, N = _wshape(w.packed_codes)
-        _arg(out, torch.float32, name, d_out.device, (E, N, w.packed_codes.shape[3] * 64),
-             optional=True)
+        if out is not None:
+            E, N = _wshape(w.packed_codes)
+            _arg(out, torch.float32, name, d_out.device, (E, N, w.packed_codes.shape[3] * 64))
     if (dw_first is None or dw_down is None) and dw_dtype not in (torch.float32, torch.bfloat16):
         raise NvfpError(f"dw_dtype must be float32 or bfloat16, not {dw_dtype}")
     with _where(d_out):

@@ -153,6 +153,7 @@ def current(monkeypatch):
         def __exit__(self, *exc):
             stack.pop()
     monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(OnDevice, "device", property(lambda t: torch.device("cuda", 1)),
                         raising=False)
     return stack
