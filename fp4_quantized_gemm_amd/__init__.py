@@ -641,7 +641,7 @@ def grouped_w4a16_dgrad(dy, dy_rows, w_codes, w_scales, g_w, expert_offsets, M_t
     """dX [M_total][K] bf16 = dy (bf16 [M_src][N], gathered by dy_rows) times
     the dequantized NVFP4 weights of each row's expert, contracted over N: the
     input gradient of grouped_w4a16_gemm.  Rows outside the experts' are left
-    as they were."""
+    as they were (uninitialised without out)."""
     if not isinstance(dy, torch.Tensor) or not dy.is_cuda:
         raise NvfpError("dy must be a device tensor")
     dev = dy.device
@@ -707,7 +707,8 @@ def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h
     [gate | up] bf16, or a checkpoint's codes with y_scales; dh [P][I] bf16 is
     h's gradient without the routing weight; inv_perm [T][tk] i32 and topk_w
     [T][tk] f32 as moe_permute returns them (both None: one slot per row,
-    weight 1)."""
+    weight 1).  inv_perm is a permutation of the rows: an entry out of range is
+    skipped, and what it would have written stays uninitialised."""
     dev = getattr(y, "device", None)
     yp = _arg(y, torch.bfloat16 if y_scales is None else torch.uint8, "y", dev, (None, None))
     P, I2 = y.shape

@@ -197,12 +197,14 @@ __device__ __forceinline__ void dgrad_out(uint8_t* own, const f32x16_t (&acc)[2]
 // (32768 skewed rows 0.280 -> 0.261 ms, 16384 rows over 128 experts of
 // 4096x1536 0.357 -> 0.308 ms).
 //
-// Measured: 131072 rows, 128 experts of 4096x1536, 1.42 to 1.47 ms = 1.15 PFLOP/s;
-// 32768 rows, 128 experts of 1536x2048 (half the experts a tile and a tail),
-// 0.25 ms.  When the first took 1.59 ms it took 1.30 without the weight decode,
-// and the matrix units were 53% busy at 1.8 GHz: the chip's power limit, then
-// LDS and vector instructions beside the products.  A persistent form (one
-// workgroup per CU) was slower, 1.57 against 1.53 ms and 0.31 against 0.28.
+// Measured: 131072 rows, 128 experts of 4096x1536, 1.43 to 1.48 ms = 1.13 PFLOP/s
+// (1.50 on a slower card); 32768 rows, 128 experts of 1536x2048 (half the
+// experts a tile and a tail), 0.25 ms.  Counters at the first: matrix units 60%
+// busy, waves waiting for LDS 13% of their time, clock 1.84 GHz; operands of
+// zeros take the same cycles at 2.38 GHz, 1.15 ms.  So the chip's power limit,
+// then LDS and the weights' decode beside the products.  An earlier form of
+// 1.53 ms was slower as one persistent workgroup per CU (1.57 ms, and 0.31
+// against 0.28 on the second).
 // ---------------------------------------------------------------------------
 namespace dg {
 constexpr int BC = 64;
@@ -466,11 +468,14 @@ k_dgrad(GradArgs p, int n_tiles) {
 // waves of a workgroup, four strips of one expert, share them in L1).  32 rows
 // of the expert per pass; more re-stream the weights.
 //
-// Measured: 2048 rows over 128 experts of 4096x1536, 115 us = 4.0 TB/s of
-// weights (161 us tile by tile); one row of one such expert 20 us.  Bound by
-// its vector instructions (two per decoded weight, 16 per 8) and their issue,
-// with three waves per SIMD; with up to 64 rows per pass and two waves per SIMD
-// 146 us.
+// Measured: 2048 rows over 128 experts of 4096x1536, evenly routed (26 rows in
+// the longest expert), 115 us = 4.0 TB/s of weights (161 us tile by tile); one
+// row of one such expert 20 us.  Bound by its vector instructions (two per
+// decoded weight, 16 per 8) and their issue, with three waves per SIMD; with up
+// to 64 rows per pass and two waves per SIMD 146 us.  The passes of an expert
+// follow one another, about 55 us each there, so uneven routing costs: 216 us
+// with 94 rows in the longest expert, 444 with 171, 1.9 ms with half of all
+// rows in one, 3.6 with all.
 // ---------------------------------------------------------------------------
 namespace dgf {
 constexpr int BC = 64;
@@ -677,13 +682,15 @@ struct WgStep {
   uint32_t p, hi, a0, b0;
 };
 
-// Measured: 131072 rows, 128 experts of 4096x1536, bf16 dw, 1.54 ms = 1.07
-// PFLOP/s (1.35 ms without the stores; 0.97 ms with operands of zeros, at the
-// full clock): bound by the chip's power limit at these operands (1.5 to 1.7
-// GHz, matrix units 64% busy).  32768 rows from 8-bit x, 128 experts of
-// 1536x2048, float32 dw (1.6 GB), 0.48 ms, 0.25 ms without the stores: bound by
-// the stores (5.5 TB/s with nothing else running) and operands that come from
-// memory beside them.
+// Measured: 131072 rows, 128 experts of 4096x1536, bf16 dw, 1.51 to 1.55 ms =
+// 1.07 PFLOP/s.  Counters: matrix units 64% busy at 1.68 GHz; operands of zeros
+// take 10% more cycles at 2.38 GHz, 1.18 ms: bound by the chip's power limit at
+// real operands, then by waits.  There with float32 dw 1.71 to 1.73 ms, added to
+// 2.14 to 2.17; 8-bit x the same within 3%.  32768 rows from 8-bit x, 128
+// experts of 1536x2048, float32 dw (1.6 GB), 0.48 ms with new inputs each time
+// (0.34 where they fit the Infinity Cache), added to 0.64: bound by the stores
+// (5.5 TB/s with nothing else running) and operands that come from memory
+// beside them.
 // MX: x is an 8-bit checkpoint.  LA, LB: dy, x are gathered through a row list
 // (without one a row is its step's own, and no per-row arithmetic is left).
 template <bool MX, bool LA, bool LB>
@@ -1083,8 +1090,9 @@ static bool wgrad_sizes(int64_t E, int64_t M_total, int64_t N, int64_t K) {
          N <= (1LL << 20) && K >= 8 && K % 8 == 0 && K <= (1LL << 20);
 }
 
-// The input gradient's few-row kernel: up to 16 rows per expert on average,
-// routed at random (128 experts of 1536x2048: 68 against 87 us at 16 rows, 97
+// The input gradient's few-row kernel: up to 16 rows per expert on average
+// (the host knows no more; the kernel's comment has what uneven rows cost),
+// measured routed at random (128 experts of 1536x2048: 68 against 87 us at 16 rows, 97
 // against 92 at 24, 119 against 101 at 32; 8 of 4096x4096: 35 against 34 at
 // 16, 43 against 34 at 24), or 64 rows in all (one expert of 4096x1536, 64
 // rows: 15 against 18 us, 100 rows 31 against 22).

@@ -58,8 +58,8 @@ __device__ __forceinline__ uint2 mx_encode8(const uint4& v, uint32_t& sbyte) {
 }
 
 // One lane per 8 columns (GLU: per 8 gate columns and the same up columns),
-// one pass: 2 bytes read and 1.03 written per element, 3 of h's besides.  Bound
-// by memory: with the restore behind it 73 us for 16384x4096 (5.6 TB/s of both
+// one pass: 2 bytes read and 1.03 written per element, 1 more written with h.
+// Bound by memory: with the restore behind it 73 us for 16384x4096 (5.6 TB/s of both
 // together), 65 us for 32768x1536 with h; nontemporal loads and stores gained
 // 4% there, and would take h and the codes past the caches of their readers.
 // IT: index type of the flat chunk number (32 bits where it fits: the
@@ -119,8 +119,9 @@ k_restore(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
 // Backward of h = silu(g) u with the routing weight w of the row's slot:
 //   s = 1 / (1 + e^-g), dg = w dh u s (1 + g (1 - s)), du = w dh g s,
 //   hw = w g s u, dw = sum_i dh_i g_i s_i u_i
-// all in float32 (hardware exp2 and reciprocal, a few ulps), one rounding to
-// bf16 per output.  One wave per (token, slot), one pass: bound by memory, 265
+// all in float32 (hardware exp2 and reciprocal, a few ulps; a reciprocal below
+// 2^-126 comes out as 0, here as in the forward), one rounding to bf16 per
+// output.  One wave per (token, slot), one pass: bound by memory, 265
 // us for 131072 rows of 1024 from 8-bit y (5.1 TB/s, a plain copy's rate); the
 // nontemporal forms of its loads and stores measured the same.
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dh, float w, float& dg,

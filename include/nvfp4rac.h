@@ -460,7 +460,8 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
  * y [T*tk][2I] = [gate | up] bf16, or the codes of its checkpoint with
  * y_scales [T*tk][2I/32]; dh [T*tk][I] bf16, the gradient of h with the
  * routing weight left out (the input gradient of the down product, of
- * d_out[t] itself).  With s = 1 / (1 + e^-gate), in float32:
+ * d_out[t] itself).  With s = 1 / (1 + e^-gate), in float32 (0 where s is
+ * below 2^-126, at gates under -87.3, as in the forward):
  *   dy[p] = [ w dh up s (1 + gate (1 - s)) | w dh gate s ]   bf16 [T*tk][2I]
  *   hw[p] = w gate s up                  bf16 [T*tk][I] or NULL (the x of the
  *           down product's grouped_wgrad, whose dy is d_out itself)
