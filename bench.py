@@ -767,6 +767,12 @@ def gemm_algorithmic_bytes(cfg, counts):
     return total
 
 
+def four_digits(v):
+    """v to four significant digits: of a small workload a few decimals may
+    leave zero."""
+    return float(f"{v:.4g}")
+
+
 def roofline_of(cfg, res, decode):
     """The grouped GEMM calls of a step against their bound: MFMA (f16/bf16
     dense peak) for prefill, HBM for decode-sized blocks."""
@@ -909,8 +915,8 @@ def main():
         if c16 and line["roofline"]["bound"] == "mfma":
             # the same achieved rate against the f16 matrix-core rate on
             # this workload's own NVFP4 operand values
-            line["roofline"]["frac_of_f16_rate_on_these_operands"] = round(
-                line["roofline"]["achieved"] / c16, 4)
+            line["roofline"]["frac_of_f16_rate_on_these_operands"] = four_digits(
+                line["roofline"]["achieved"] / c16)
     gates = {}
     r = line["roofline"]
     if r["bound"] == "mfma":
