@@ -129,12 +129,13 @@ class TrainState:
 def _check_block(x, logits, bias, w_first, w_down):
     """The operands of a block fit together: the products take their sizes
     from one operand and index the others with them on the device."""
-    if not x.is_cuda or x.dtype is not torch.bfloat16 or x.dim() != 2:
-        _arg(x, torch.bfloat16, "x", x.device, (None, None))
+    dev = getattr(x, "device", None)
+    if not getattr(x, "is_cuda", False) or x.dtype is not torch.bfloat16 or x.dim() != 2:
+        _arg(x, torch.bfloat16, "x", dev, (None, None))
     T, H = x.shape
-    if logits.dim() != 2 or logits.shape[0] != T:
-        raise NvfpError(f"logits must have shape [{T}, None], got {list(logits.shape)}")
-    dev, E = x.device, logits.shape[1]
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[0] != T:
+        _arg(logits, torch.float32, "logits", dev, (T, None))
+    E = logits.shape[1]
     if bias is not None:
         _arg(bias, torch.float32, "bias", dev)
         if bias.numel() != E:
@@ -208,8 +209,8 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     down projection's products as it is, gathered by token."""
     # (d_out is gathered by token, a token past its end as its last row)
     T, H = st.topk_w.shape[0], st.w_down.packed_codes.shape[2] * 16
-    if d_out.shape != (T, H):
-        raise NvfpError(f"d_out must have shape {[T, H]}, got {list(d_out.shape)}")
+    if getattr(d_out, "shape", None) != (T, H):
+        raise NvfpError(f"d_out must be a device tensor of shape {[T, H]}")
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
     # which has twice the columns: it comes first)

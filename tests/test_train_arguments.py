@@ -175,3 +175,15 @@ def test_a_step_runs_with_its_tensors_device_current(calls, current, monkeypatch
     with pytest.raises(F.NvfpError):
         forward(x=there(T - 1, H))
     assert current == ["cuda:0"]
+
+
+@pytest.mark.parametrize("bad", [None, 3.0, [[1.0]]])
+def test_what_is_no_tensor_is_refused_like_the_rest(calls, bad):
+    with pytest.raises(F.NvfpError, match="d_out"):
+        pipeline.moe_train_backward(state(), bad)
+    with pytest.raises(F.NvfpError, match="x must"):
+        pipeline.moe_train_forward(bad, there(T, E, dtype=F32), TK, weights(E, 2 * I, H),
+                                   weights(E, H, I))
+    with pytest.raises(F.NvfpError, match="logits must"):
+        pipeline.moe_train_forward(there(T, H), bad, TK, weights(E, 2 * I, H), weights(E, H, I))
+    assert not calls
