@@ -23,6 +23,12 @@ and the training step around the W4A16 product: 8-bit activation checkpoints,
 the product's input and weight gradients, the SwiGLU's backward pass,
     mxfp8_checkpoint, mxfp8_restore, grouped_w4a16_dgrad, grouped_wgrad,
     moe_swiglu_backward
+and microscaled 4-bit operands (MXFP4), which the matrix cores multiply
+natively, with their expert product,
+    mxfp4_quantize, mxfp4_restore, grouped_mxfp4_gemm, grouped_mxfp4_gemm_swiglu
+and the gradients of the routing: of the weighted combine, and of the softmax
+over the chosen experts,
+    moe_unpermute_combine_backward, moe_permute_backward
 """
 from __future__ import annotations
 
@@ -41,7 +47,9 @@ __all__ = ["lib", "nvfp4_qdq_weights", "nvfp4_pack_weights", "QdqWeights",
            "grouped_w4a4_gemm_rac_per_expert", "grouped_w4a4_gemm_rac_swiglu",
            "nvfp4_quantize_act_amax", "fp8_quantize", "grouped_fp8_gemm",
            "mxfp8_checkpoint", "mxfp8_restore", "grouped_w4a16_dgrad", "grouped_wgrad",
-           "moe_swiglu_backward", "NvfpError", "EXPORTED_SYMBOLS"]
+           "moe_swiglu_backward", "mxfp4_quantize", "mxfp4_restore", "grouped_mxfp4_gemm",
+           "grouped_mxfp4_gemm_swiglu", "moe_unpermute_combine_backward", "moe_permute_backward",
+           "NvfpError", "EXPORTED_SYMBOLS"]
 
 EXPORTED_SYMBOLS = [
     "nvfp4_version", "nvfp4_status_str", "nvfp4_last_error",
@@ -64,6 +72,10 @@ EXPORTED_SYMBOLS = [
     "grouped_w4a16_dgrad_workspace_size", "grouped_w4a16_dgrad",
     "grouped_wgrad_workspace_size", "grouped_wgrad",
     "moe_swiglu_backward",
+    "mxfp4_quantize", "mxfp4_quantize_transposed", "mxfp4_restore",
+    "grouped_mxfp4_gemm_workspace_size", "grouped_mxfp4_gemm", "grouped_mxfp4_gemm_swiglu",
+    "moe_unpermute_combine_backward",
+    "moe_permute_backward_workspace_size", "moe_permute_backward",
 ]
 
 
@@ -107,6 +119,8 @@ def _load():
         "grouped_fp8_gemm_workspace_size": [_I64],
         "grouped_w4a16_dgrad_workspace_size": [_I64, _I64, _I64, _I64],
         "grouped_wgrad_workspace_size": [_I64, _I64, _I64, _I64],
+        "grouped_mxfp4_gemm_workspace_size": [_I64, _I64, _I64, _I64],
+        "moe_permute_backward_workspace_size": [_I64, _I64],
     }.items():
         f = getattr(L, name)
         f.restype = _SZ
@@ -141,6 +155,15 @@ def _load():
         "grouped_wgrad": [_P, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64, _I64, _I64, _P,
                           ctypes.c_int, ctypes.c_int, _P, _SZ, _P],
         "moe_swiglu_backward": [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P],
+        "mxfp4_quantize": [_P, _I64, _I64, _I64, _P, _P, _P],
+        "mxfp4_quantize_transposed": [_P, _I64, _I64, _I64, _I64, _P, _P, _P],
+        "mxfp4_restore": [_P, _P, _I64, _I64, _P, _I64, _P],
+        "grouped_mxfp4_gemm": [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _SZ,
+                               _P],
+        "grouped_mxfp4_gemm_swiglu": [_P, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P,
+                                      _SZ, _P],
+        "moe_unpermute_combine_backward": [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P],
+        "moe_permute_backward": [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P],
     }
     for name, args in sigs.items():
         f = getattr(L, name)
@@ -733,3 +756,143 @@ def moe_swiglu_backward(y, dh, inv_perm=None, topk_w=None, y_scales=None, want_h
         dwp = dw.data_ptr()
     _call("moe_swiglu_backward", dev, yp, sp, dhp, ip, wp, T, tk, I, dy.data_ptr(), hp, dwp)
     return dy, hw, dw
+
+
+def _device_of(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise NvfpError(f"{name} must be a device tensor")
+    return t.device
+
+
+def mxfp4_quantize(x, transpose=False):
+    """MXFP4 codes and scales of x [M][K] bf16 (rows may be strided) or of
+    stacked weights [E][N][K] (contiguous) -> (codes u8 [..][K/2], scales u8
+    E8M0 [..][K/32]), blocks of 32 along the last dimension.  transpose=True:
+    of the transpose of x, or of each x[e], with blocks along x's rows: [..]
+    [K][M/2] and [..][K][M/32]."""
+    dev = _device_of(x, "x")
+    if x.dim() == 3:
+        xp = _arg(x, torch.bfloat16, "x", dev)
+        E, M, K = x.shape
+        ld, lead = K, (E,)
+    else:
+        xp = _arg(x, torch.bfloat16, "x", dev, (None, None), strided=True)
+        (M, K), E, lead = x.shape, 1, ()
+        ld = _ld(x)
+    rows, cols = (K, M) if transpose else (M, K)
+    codes = torch.empty(lead + (rows, cols // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty(lead + (rows, cols // 32), dtype=torch.uint8, device=dev)
+    if transpose:
+        _call("mxfp4_quantize_transposed", dev, xp, E, M, K, ld, codes.data_ptr(),
+              scales.data_ptr())
+    else:
+        _call("mxfp4_quantize", dev, xp, E * M, K, ld, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def mxfp4_restore(codes, scales, out=None):
+    """The bf16 values [..][K] that MXFP4 codes [..][K/2] and scales [..][K/32]
+    stand for (exact; [M][K] or [E][N][K]).  out: a bf16 tensor to write; of a
+    2-D one the rows may be strided."""
+    dev = _device_of(codes, "codes")
+    cp = _arg(codes, torch.uint8, "codes", dev, None if codes.dim() == 3 else (None, None))
+    shape = tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
+    sp = _arg(scales, torch.uint8, "scales", dev, shape[:-1] + (shape[-1] // 32,))
+    xp = _arg(out, torch.bfloat16, "out", dev, shape, optional=True, strided=len(shape) == 2)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        xp = out.data_ptr()
+    rows = shape[0] if len(shape) == 2 else shape[0] * shape[1]
+    _call("mxfp4_restore", dev, cp, sp, rows, shape[-1], xp,
+          _ld(out) if len(shape) == 2 else shape[-1])
+    return out
+
+
+def _mxfp4_gemm(name, a_codes, a_scales, a_rows, w_codes, w_scales, expert_offsets, M_total, out,
+                glu):
+    dev = _device_of(a_codes, "a_codes")
+    wp = _arg(w_codes, torch.uint8, "w_codes", dev, (None, None, None))
+    E, N, half = w_codes.shape
+    K = 2 * half
+    wsp = _arg(w_scales, torch.uint8, "w_scales", dev, (E, N, K // 32))
+    ap = _arg(a_codes, torch.uint8, "a_codes", dev, (None, half))
+    M_src = a_codes.shape[0]
+    asp = _arg(a_scales, torch.uint8, "a_scales", dev, (M_src, K // 32))
+    rp = _arg(a_rows, torch.int32, "a_rows", dev, (None,), optional=True)
+    op = _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
+    M_total = _m_total(M_total, M_src, a_rows)
+    cols = N // 2 if glu else N
+    yp = _arg(out, torch.bfloat16, "out", dev, (M_total, cols), optional=True)
+    if out is None:
+        out = torch.empty((M_total, cols), dtype=torch.bfloat16, device=dev)
+        yp = out.data_ptr()
+    nb = (_lib or _load()).grouped_mxfp4_gemm_workspace_size(E, M_total, N, K)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _call(name, dev, ap, asp, rp, M_src, wp, wsp, op, E, M_total, N, K, yp, ws.data_ptr(), nb)
+    return out
+
+
+def grouped_mxfp4_gemm(a_codes, a_scales, a_rows, w_codes, w_scales, expert_offsets, M_total=None,
+                       out=None):
+    """Y [M_total][N] bf16 = the MXFP4 rows a_codes [M_src][K/2], a_scales
+    [M_src][K/32] (gathered by a_rows) times the MXFP4 weights w_codes
+    [E][N][K/2], w_scales [E][N][K/32] of each row's expert, as mxfp4_quantize
+    returns both.  Rows outside the experts' are left as they were
+    (uninitialised without out)."""
+    return _mxfp4_gemm("grouped_mxfp4_gemm", a_codes, a_scales, a_rows, w_codes, w_scales,
+                       expert_offsets, M_total, out, False)
+
+
+def grouped_mxfp4_gemm_swiglu(a_codes, a_scales, a_rows, w_codes, w_scales, expert_offsets,
+                              M_total=None, out=None):
+    """h [M_total][N/2] bf16 = SwiGLU of grouped_mxfp4_gemm, whose weights' N
+    rows are [gate | up], from its float32 sums."""
+    return _mxfp4_gemm("grouped_mxfp4_gemm_swiglu", a_codes, a_scales, a_rows, w_codes, w_scales,
+                       expert_offsets, M_total, out, True)
+
+
+def moe_unpermute_combine_backward(d_out, y, inv_perm, topk_w):
+    """Gradient of moe_unpermute_combine for d_out [T][N] bf16 -> (dy [T*tk][N]
+    bf16 by permuted row, d_topk_w [T][tk] f32).  y [T*tk][N] bf16 is the
+    combine's input (None: d_topk_w is None); inv_perm, topk_w [T][tk] as
+    moe_permute returns them.  inv_perm is a permutation of the rows: an entry
+    out of range is skipped, and what it would have written stays
+    uninitialised."""
+    dev = _device_of(d_out, "d_out")
+    dp = _arg(d_out, torch.bfloat16, "d_out", dev, (None, None))
+    T, N = d_out.shape
+    ip = _arg(inv_perm, torch.int32, "inv_perm", dev, (T, None))
+    tk = inv_perm.shape[1]
+    wp = _arg(topk_w, torch.float32, "topk_w", dev, (T, tk))
+    yp = _arg(y, torch.bfloat16, "y", dev, (T * tk, N), optional=True)
+    dy = torch.empty((T * tk, N), dtype=torch.bfloat16, device=dev)
+    dw = dwp = None
+    if y is not None:
+        dw = torch.empty((T, tk), dtype=torch.float32, device=dev)
+        dwp = dw.data_ptr()
+    _call("moe_unpermute_combine_backward", dev, dp, yp, ip, wp, T, tk, N, dy.data_ptr(), dwp)
+    return dy, dw
+
+
+def moe_permute_backward(topk_ids, topk_w, d_topk_w, E, want_bias=False):
+    """Gradient of moe_permute's routing weights -> (d_logits [T][E] f32, d_bias
+    [E] f32 or None without want_bias): the softmax over the chosen experts, 0
+    for the others.  topk_ids [T][tk] i32 and topk_w [T][tk] f32 as moe_permute
+    returns them, d_topk_w [T][tk] f32."""
+    dev = _device_of(topk_ids, "topk_ids")
+    ip = _arg(topk_ids, torch.int32, "topk_ids", dev, (None, None))
+    T, tk = topk_ids.shape
+    wp = _arg(topk_w, torch.float32, "topk_w", dev, (T, tk))
+    dwp = _arg(d_topk_w, torch.float32, "d_topk_w", dev, (T, tk))
+    if not isinstance(E, int) or not 1 <= E <= 1024:
+        raise NvfpError(f"E must be from 1 to 1024, not {E!r}")
+    dl = torch.empty((T, E), dtype=torch.float32, device=dev)
+    db = ws = dbp = wsp = None
+    nb = 0
+    if want_bias:
+        db = torch.empty(E, dtype=torch.float32, device=dev)
+        nb = (_lib or _load()).moe_permute_backward_workspace_size(T, E)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        dbp, wsp = db.data_ptr(), ws.data_ptr()
+    _call("moe_permute_backward", dev, ip, wp, dwp, T, E, tk, dl.data_ptr(), dbp, wsp, nb)
+    return dl, db

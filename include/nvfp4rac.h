@@ -477,6 +477,98 @@ int moe_swiglu_backward(const void* y, const uint8_t* y_scales, const void* dh,
                         const int32_t* inv_perm, const float* topk_w, int64_t T, int64_t tk,
                         int64_t I, void* dy, void* hw, float* d_topk_w, void* stream);
 
+/* ------------------------------------------------------------------------
+ * OCP MXFP4, the 4-bit format that CDNA4's matrix cores multiply natively: the
+ * same E2M1 codes as above, packed two per byte, with one E8M0 byte
+ * (2^(byte - 127), 255 = NaN) per 32 consecutive elements and no tensor scale.
+ * (The pages name only FP4's E2M1 grid and "fine-grained scaling": abstract;
+ * gist.science summary §1.)
+ *
+ * Scale of a block with largest magnitude A: the smallest power of two 2^E
+ * with A <= 7 * 2^E, E kept within -125 .. 125 (-125 for a block of zeros), so
+ * that every value is a normal bf16 or 0.  code = E2M1(x * 2^-E), round to
+ * nearest, ties to the even code, saturating at 6; the sign bit is the sign of
+ * x.  A block that holds a NaN or an infinity is NaN as a whole: byte 255,
+ * codes 7.
+ *
+ * mxfp4_quantize: x [M][K] bf16, row stride ldx elements -> codes [M][K/2],
+ *   scales [M][K/32], row-major.  Weights [E][N][K] are E * N rows.  Requires
+ *   0 <= M < 2^40, K % 32 == 0, 32 <= K <= ldx < 2^22, ldx % 8 == 0; x and
+ *   codes 16-byte, scales unaligned.  No workspace.
+ * mxfp4_quantize_transposed: the same for the transpose of each of E matrices
+ *   x [M][K] (row stride ldx, matrices M * ldx apart): blocks of 32 rows of x
+ *   -> codes [E][K][M/2], scales [E][K][M/32], the operand of a product that
+ *   contracts over the rows (the input gradient's weights).  Requires
+ *   0 <= E < 65536, M % 32 == 0, 32 <= M < 2^22, K % 8 == 0, 8 <= K <= ldx <
+ *   2^22, ldx % 8 == 0; alignment as above.  No workspace.
+ * mxfp4_restore: x [M][K] bf16 (row stride ldx) = code * 2^(byte - 127),
+ *   exactly, for every byte whose values bf16 holds (1 .. 252: all of them),
+ *   NaN for 255.  Limits and alignment as mxfp4_quantize.  No workspace.
+ * ---------------------------------------------------------------------- */
+int mxfp4_quantize(const void* x, int64_t M, int64_t K, int64_t ldx, uint8_t* codes,
+                   uint8_t* scales, void* stream);
+int mxfp4_quantize_transposed(const void* x, int64_t E, int64_t M, int64_t K, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, void* stream);
+int mxfp4_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, void* x,
+                  int64_t ldx, void* stream);
+
+/* Expert-grouped product of MXFP4 operands.  a_codes [M_src][K/2], a_scales
+ * [M_src][K/32]; w_codes [E][N][K/2], w_scales [E][N][K/32], all row-major as
+ * mxfp4_quantize writes them; a_rows [M_total] or NULL (identity).  For output
+ * row p of expert e, t = a_rows ? a_rows[p] : p:
+ *   y[p][n] = bf16( sum over blocks b of 2^(sa[t][b] + sw[e][n][b] - 254)
+ *                   sum_{k in b} a[t][k] w[e][n][k] )
+ * (exact products, float32 accumulation, one rounding).  y [M_total][N] bf16;
+ * rows outside [off[0], off[E]) are left as they were; y overlaps no input.
+ * The input gradient is the same call with dy quantised along N and the
+ * weights of mxfp4_quantize_transposed.
+ * _swiglu: the weights' rows are [gate | up]; h [M_total][N/2] = bf16(silu(
+ * gate) * up) of the float32 sums (s = 1 / (1 + e^-gate), 0 where s is below
+ * 2^-126, at gates under -87.3).
+ * Requires 1 <= E <= 1024, 0 <= M_total < 2^31, N % 16 == 0 (_swiglu:
+ * N % 32 == 0), K % 128 == 0, N and K <= 2^20, the activation's codes and one
+ * expert's below 4 GiB; codes, y and ws 16-byte, scales 4-byte aligned; a_rows
+ * NULL needs M_src >= M_total.  a_rows entries outside [0, M_src) read its
+ * first or last row. */
+size_t grouped_mxfp4_gemm_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
+int grouped_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* a_rows,
+                       int64_t M_src, const uint8_t* w_codes, const uint8_t* w_scales,
+                       const int32_t* expert_offsets, int64_t E, int64_t M_total, int64_t N,
+                       int64_t K, void* y, void* ws, size_t ws_bytes, void* stream);
+int grouped_mxfp4_gemm_swiglu(const uint8_t* a_codes, const uint8_t* a_scales,
+                              const int32_t* a_rows, int64_t M_src, const uint8_t* w_codes,
+                              const uint8_t* w_scales, const int32_t* expert_offsets, int64_t E,
+                              int64_t M_total, int64_t N, int64_t K, void* h, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Gradient of moe_unpermute_combine.  d_out [T][N] bf16; for slot (t, j) with
+ * row p = inv_perm[t][j]:
+ *   dy[p][n] = bf16( topk_w[t][j] * d_out[t][n] )            [T*tk][N] bf16
+ *   d_topk_w[t][j] = sum_n d_out[t][n] * y[p][n], float32    [T][tk]
+ * y [T*tk][N] bf16 and d_topk_w are both there or both NULL.  inv_perm is a
+ * permutation; an entry outside [0, T*tk) is skipped: its d_topk_w, and the
+ * rows that no entry names, are left as they were.  No output overlaps an
+ * input.  Requires 1 <= tk <= 32, T*tk < 2^31, N % 8 == 0, 8 <= N < 2^31;
+ * d_out, y and dy 16-byte aligned.  No workspace. */
+int moe_unpermute_combine_backward(const void* d_out, const void* y, const int32_t* inv_perm,
+                                   const float* topk_w, int64_t T, int64_t tk, int64_t N, void* dy,
+                                   float* d_topk_w, void* stream);
+
+/* Gradient of moe_permute's routing weights, the softmax over the tk chosen
+ * experts of l = logit + bias:
+ *   d_logits[t][topk_ids[t][j]] = w_j (dw_j - sum_i w_i dw_i),  w = topk_w[t],
+ *   dw = d_topk_w[t]; 0 for the experts not chosen           [T][E] float32
+ *   d_bias[e] = sum_t d_logits[t][e]                [E] float32, or NULL
+ * in float32 (d_bias: parts of up to 4 ceil(T/4096) tokens in float32, then
+ * float64), in an order that does not depend on timing.  An expert that a token
+ * names twice gets the sum of both; ids outside [0, E) write nothing.
+ * Requires T >= 0, 1 <= tk <= min(E, 32), E <= 1024, T*tk < 2^31.  T == 0
+ * writes d_bias = 0 only.  ws is needed with d_bias alone. */
+size_t moe_permute_backward_workspace_size(int64_t T, int64_t E);
+int moe_permute_backward(const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
+                         int64_t T, int64_t E, int64_t tk, float* d_logits, float* d_bias,
+                         void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

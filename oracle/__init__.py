@@ -18,9 +18,11 @@ Modules:
            expert-grouped product
   train    8-bit activation checkpoints, the gradients of the W4A16 product
            and of the SwiGLU with its routing weights
+  mxfp4    MXFP4 quantization and expert-grouped product, the gradients of the
+           combine and of the routing
 
 Every function is pinned by tests under tests/ against facts that do not come
 from the oracle itself (bit definitions, exact rational arithmetic, library
 routines, closed forms and invariants).
 """
-from . import formats, fp8, gemm, layer, moe, nvfp4, train  # noqa: F401
+from . import formats, fp8, gemm, layer, moe, mxfp4, nvfp4, train  # noqa: F401
