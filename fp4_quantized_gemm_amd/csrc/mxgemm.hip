@@ -160,10 +160,13 @@ constexpr int BM = 128, BN = 256, BK = 128;
 constexpr int A_BYTES = BM * 64, STAGE = (BM + BN) * 64;
 }  // namespace mxb
 
-// prefix[e] = row tiles of the experts before e, prefix[E] = all
+// The row tiles of all experts, in order: tiles[t] = {expert, first row, rows,
+// 0}, and their number.  Every workgroup sums the experts' tiles for itself and
+// writes a part of the list.
 __global__ void __launch_bounds__(1024)
-k_mx_tiles(MxGemmArgs p, int32_t* __restrict__ prefix) {
+k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
   __shared__ int wsum[16];
+  __shared__ int prefix[1025];
   const int tid = threadIdx.x;
   int v = 0;
   if (tid < p.E) {
@@ -180,8 +183,22 @@ k_mx_tiles(MxGemmArgs p, int32_t* __restrict__ prefix) {
   __syncthreads();
   int base = 0;
   for (int w = 0; w < (tid >> 6); ++w) base += wsum[w];
-  if (tid < p.E) prefix[tid] = base + incl - v;
-  if (tid == p.E - 1) prefix[p.E] = base + incl;
+  prefix[tid] = base + incl - v;
+  if (tid == 1023) prefix[1024] = base + incl;
+  __syncthreads();
+  const int total = prefix[1024];
+  for (int t = blockIdx.x * 1024 + tid; t < total; t += gridDim.x * 1024) {
+    int lo_e = 0, hi_e = p.E;                            // largest e with prefix[e] <= t
+    while (hi_e - lo_e > 1) {
+      const int mid = (lo_e + hi_e) >> 1;
+      if (prefix[mid] <= t) lo_e = mid; else hi_e = mid;
+    }
+    int64_t lo, hi;
+    expert_rows(p, lo_e, lo, hi);
+    const int64_t p0 = lo + (int64_t)(t - prefix[lo_e]) * mxb::BM;
+    tiles[t] = make_int4(lo_e, (int)p0, (int)(hi - p0 < mxb::BM ? hi - p0 : mxb::BM), 0);
+  }
+  if (blockIdx.x == 0 && tid == 0) *n_tiles = total;
 }
 
 // D += 2^(sa - 127 + sb - 127) A B over 64 k: lane (r = l % 32, q = l / 32)
@@ -196,7 +213,8 @@ __device__ __forceinline__ f32x16_t mfma32_mx4(const u32x4& a, uint32_t sa, cons
 
 template <bool GLU>
 __global__ void __launch_bounds__(256, 2)
-k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_tiles) {
+k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict__ n_row_tiles,
+         int n_tiles) {
   using namespace mxb;
   // separate objects, and the ring unrolled: each access names its stage, so
   // the compiler does not wait for loads into the others
@@ -210,7 +228,7 @@ k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_ti
   // groups of 8 row tiles x all column tiles; each XCD (workgroup b runs on
   // XCD b % 8) takes a contiguous range, so its L2 holds an expert's weights
   constexpr int G = 8;
-  const int real_m = __builtin_amdgcn_readfirstlane(prefix[p.E]);
+  const int real_m = *n_row_tiles;
   const int total = real_m * n_tiles;
   const int per_xcd = (total + 7) / 8;
   const int loc = (int)blockIdx.x >> 3;
@@ -219,17 +237,10 @@ k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_ti
   if (v >= total) return;
   const int gi = v / (G * n_tiles), gr = v - gi * G * n_tiles;
   const int gm = real_m - G * gi < G ? real_m - G * gi : G;
-  const int nt = gr / gm, gt = G * gi + gr - nt * gm;
-  int lo_e = 0, hi_e = p.E;                              // largest e with prefix[e] <= gt
-  while (hi_e - lo_e > 1) {
-    const int mid = (lo_e + hi_e) >> 1;
-    if (prefix[mid] <= gt) lo_e = mid; else hi_e = mid;
-  }
-  const int e = lo_e;
-  int64_t e_lo, e_hi;
-  expert_rows(p, e, e_lo, e_hi);
-  const int64_t p0 = e_lo + (int64_t)(gt - prefix[e]) * BM;
-  const int valid = (int)(e_hi - p0 < BM ? e_hi - p0 : BM);
+  const int nt = gr / gm;
+  const int4 tile = tiles[G * gi + gr - nt * gm];
+  const int e = tile.x, valid = tile.z;
+  const int64_t p0 = tile.y;
   if (tid < BM) rows_src[tid] = (int32_t)source_row(p, p0 + (tid < valid ? tid : valid - 1));
   __syncthreads();
 
@@ -303,9 +314,14 @@ k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_ti
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  const int swz = (r32 >> 2) & 3;
-  auto ld = [&](const uint8_t* base, int row, int c) -> u32x4 {
-    return *reinterpret_cast<const u32x4*>(base + row * 64 + ((c ^ swz) << 4));
+  // (one offset per read: the compiler follows short address chains only when
+  // it decides which loads into LDS a read has to wait for)
+  const uint32_t place[2] = {(uint32_t)(r32 * 64 + (((2 * q) ^ ((r32 >> 2) & 3)) << 4)),
+                             (uint32_t)(r32 * 64 + (((2 * q + 1) ^ ((r32 >> 2) & 3)) << 4))};
+  const uint32_t w_place[2] = {place[0] + (uint32_t)(A_BYTES + 4096 * wave),
+                               place[1] + (uint32_t)(A_BYTES + 4096 * wave)};
+  auto ld = [&](const uint8_t* st, uint32_t off) -> u32x4 {
+    return *reinterpret_cast<const u32x4*>(st + off);
   };
 
   auto run = [&](auto nv_c) {
@@ -317,23 +333,25 @@ k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_ti
       constexpr bool FULL = decltype(full_c)::value;
       // all but the newest stage's loads are there; every wave is past the
       // stage that is filled next
-      if (FULL || kt + 1 < nk) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (FULL || kt + 1 < nk) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
       uint32_t tw[2], ta[NV];
 #pragma unroll
       for (int i = 0; i < 2; ++i) tw[i] = sw[i][SUB] >> (16 * q);
 #pragma unroll
       for (int j = 0; j < NV; ++j) ta[j] = sa[j][SUB] >> (16 * q);
       if (SUB == 2 && (FULL || kt + 1 < nk)) load_scales(kt + 1, full_c);
+      asm volatile("" ::: "memory");                     // (older than the stage's loads)
       if (FULL || kt + 2 < nk) issue_loads(next, kt + 2);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         u32x4 W[2], A[NV];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) W[i] = ld(st + A_BYTES, 64 * wave + 32 * i + r32, 2 * q + s);
+        for (int i = 0; i < 2; ++i) W[i] = ld(st, w_place[s] + 2048u * i);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) A[j] = ld(st, 32 * j + r32, 2 * q + s);
+        for (int j = 0; j < NV; ++j) A[j] = ld(st, place[s] + 2048u * j);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -400,6 +418,11 @@ k_mx_big(MxGemmArgs p, const int32_t* __restrict__ prefix, int n_tiles, int m_ti
 
 using namespace nvfp4;
 
+// row tiles of 128 that the experts' rows can make
+static int64_t mx_row_tiles(int64_t E, int64_t M_total) {
+  return (M_total + mxb::BM - 1) / mxb::BM + E;
+}
+
 static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uint8_t* a_scales,
                    const int32_t* a_rows, int64_t M_src, const uint8_t* w_codes,
                    const uint8_t* w_scales, const int32_t* expert_offsets, int64_t E,
@@ -432,16 +455,17 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
   hipStream_t s = as_stream(stream);
   const int64_t NO = glu ? N / 2 : N;
   if (M_total > 32 * E) {
-    int32_t* prefix = static_cast<int32_t*>(ws);
-    const int64_t n_tiles = (N + mxb::BN - 1) / mxb::BN;
-    const int64_t m_tiles = (M_total + mxb::BM - 1) / mxb::BM + E;
+    const int64_t n_tiles = (N + mxb::BN - 1) / mxb::BN, m_tiles = mx_row_tiles(E, M_total);
     NV_REQUIRE(m_tiles * n_tiles < (1 << 24), NVFP4_ERR_UNSUPPORTED, "%s: too many tiles", name);
+    int32_t* count = static_cast<int32_t*>(ws);
+    int4* tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + 256);
     const unsigned nb = (unsigned)((m_tiles * n_tiles + 7) / 8 * 8);
-    k_mx_tiles<<<1, 1024, 0, s>>>(p, prefix);
+    const int64_t tb = (m_tiles + 1023) / 1024;
+    k_mx_tiles<<<(unsigned)(tb < 256 ? tb : 256), 1024, 0, s>>>(p, tiles, count);
     if (glu)
-      k_mx_big<true><<<nb, 256, 0, s>>>(p, prefix, (int)n_tiles, (int)m_tiles);
+      k_mx_big<true><<<nb, 256, 0, s>>>(p, tiles, count, (int)n_tiles);
     else
-      k_mx_big<false><<<nb, 256, 0, s>>>(p, prefix, (int)n_tiles, (int)m_tiles);
+      k_mx_big<false><<<nb, 256, 0, s>>>(p, tiles, count, (int)n_tiles);
     return check_launch(name);
   }
   const int64_t avg = (M_total + E - 1) / E;
@@ -458,9 +482,9 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
 extern "C" {
 
 size_t grouped_mxfp4_gemm_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  (void)M_total, (void)N, (void)K;
-  if (E < 1 || E > 1024) return 256;
-  return round_up((size_t)(E + 1) * sizeof(int32_t), 256);
+  (void)N, (void)K;
+  if (E < 1 || E > 1024 || M_total < 0 || M_total >= (1LL << 31)) return 256;
+  return 256 + round_up((size_t)mx_row_tiles(E, M_total) * sizeof(int4), 256);
 }
 
 int grouped_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* a_rows,
