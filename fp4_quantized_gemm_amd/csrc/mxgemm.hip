@@ -140,24 +140,30 @@ k_mx_few(MxGemmArgs p) {
 // ------------------------------------------------------------------------
 // Large tiles: 128 activation rows x 256 weight rows per workgroup of four
 // waves, two workgroups on a CU, so one's epilogue and waits run under the
-// other's products.  Wave w owns 64 weight rows (GLU: 32 gate rows and the
-// same 32 up rows) and all of the tile's activation rows: 2 x 4 accumulators
-// of 32x32.  K advances in steps of 128 through a ring of three LDS stages,
-// filled two steps ahead by buffer loads straight into LDS.
+// other's products; a workgroup goes from tile to tile, and the loads of the
+// next tile's first step run under the last one's products.
 //
-// A stage's row is its 64 code bytes, four 16-byte pieces; piece c lies at
-// place c ^ ((row >> 2) & 3), so that the 32 rows of a fragment read without
-// bank conflicts.  Lane (r, q) of instruction s = 0, 1 takes piece 2 q + s of
-// its row, both operands alike: which 32 of the 128 columns a lane of an
-// instruction has does not matter for the sum, and so the scales of both
-// instructions are two neighbouring bytes of the row's dword.
+// Wave w owns 64 weight rows (GLU: 32 gate rows and the same 32 up rows) and
+// all of the tile's activation rows: 2 x 4 accumulators of 32x32.  K advances
+// in steps of 256, so that a row of a step is a whole 128-byte line: the
+// vector caches take as long for half a line (rows of 64 bytes reach 16 TB/s
+// from L2 into LDS, rows of 128 bytes 33).  Activation rows go through two LDS
+// stages, filled one step ahead by buffer loads straight into LDS; a weight
+// row is read by one wave only, so the weights have one stage, which the wave
+// empties into registers at the start of a step and fills again at once.
 //
-// Scales come straight to registers, three steps' (12 bytes of a row) at a
-// time.
+// A stage's row is its 128 code bytes, eight 16-byte pieces; piece c lies at
+// place c ^ ((row >> 1) & 7), so that the 32 rows of a fragment read without
+// bank conflicts.  Lane (r, q) of instruction s = 0 .. 3 takes piece 4 q + s of
+// its row, both operands alike: which 32 of the 256 columns a lane of an
+// instruction has does not matter for the sum, and so the scales of the four
+// are the bytes of one dword.  (A last step of 128 columns: s = 0, 1, piece
+// 2 q + s.)  Scales take the same way through LDS, 16 bytes of a row for two
+// steps.
 // ------------------------------------------------------------------------
 namespace mxb {
-constexpr int BM = 128, BN = 256, BK = 128;
-constexpr int A_BYTES = BM * 64, STAGE = (BM + BN) * 64;
+constexpr int BM = 128, BN = 256;
+constexpr int A_BYTES = BM * 128, W_BYTES = BN * 128, SCALES = (BM + BN) * 16;
 }  // namespace mxb
 
 // The row tiles of all experts, in order: tiles[t] = {expert, first row, rows,
@@ -211,207 +217,373 @@ __device__ __forceinline__ f32x16_t mfma32_mx4(const u32x4& a, uint32_t sa, cons
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
 }
 
-template <bool GLU>
+// all but the newest N of the wave's loads and stores are done, and its reads
+// of LDS; then every wave's
+template <int N>
+__device__ __forceinline__ void mx_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mx_barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_buffer(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
+                                           kBufferRsrcWord3);
+}
+
+struct MxTile {
+  int e, p0, valid, nt;
+};
+
+// Tile v in the order: groups of 8 row tiles x all column tiles, row tiles
+// fastest.
+__device__ __forceinline__ MxTile mx_tile(const int4* __restrict__ tiles, int real_m, int n_tiles,
+                                          int v) {
+  constexpr int G = 8;
+  const int gi = v / (G * n_tiles), gr = v - gi * G * n_tiles;
+  const int gm = real_m - G * gi < G ? real_m - G * gi : G;
+  const int nt = gr / gm;
+  const int4 t = tiles[G * gi + gr - nt * gm];
+  return {t.x, t.y, t.z, nt};
+}
+
+// ND: K / 128 modulo 4, so what the last steps are
+template <bool GLU, int ND>
 __global__ void __launch_bounds__(256, 2)
 k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict__ n_row_tiles,
          int n_tiles) {
   using namespace mxb;
-  // separate objects, and the ring unrolled: each access names its stage, so
-  // the compiler does not wait for loads into the others
-  __shared__ __attribute__((aligned(16))) uint8_t st0[STAGE], st1[STAGE], st2[STAGE];
-  __shared__ int32_t rows_src[BM];
+  // separate objects, each access naming its own: the compiler then does not
+  // wait for loads into the others
+  __shared__ __attribute__((aligned(16))) uint8_t sa0[A_BYTES], sa1[A_BYTES], sw[W_BYTES], ssc[SCALES];
+  __shared__ int32_t rows[2][BM];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 5, r32 = lane & 31;
 
-  // groups of 8 row tiles x all column tiles; each XCD (workgroup b runs on
-  // XCD b % 8) takes a contiguous range, so its L2 holds an expert's weights
-  constexpr int G = 8;
+  // each XCD (workgroup b runs on XCD b % 8) takes a contiguous range of the
+  // tiles, so its L2 holds an expert's weights; its workgroups every
+  // (gridDim / 8)-th of them
   const int real_m = *n_row_tiles;
   const int total = real_m * n_tiles;
   const int per_xcd = (total + 7) / 8;
-  const int loc = (int)blockIdx.x >> 3;
-  if (loc >= per_xcd) return;
-  const int v = ((int)blockIdx.x & 7) * per_xcd + loc;
-  if (v >= total) return;
-  const int gi = v / (G * n_tiles), gr = v - gi * G * n_tiles;
-  const int gm = real_m - G * gi < G ? real_m - G * gi : G;
-  const int nt = gr / gm;
-  const int4 tile = tiles[G * gi + gr - nt * gm];
-  const int e = tile.x, valid = tile.z;
-  const int64_t p0 = tile.y;
-  if (tid < BM) rows_src[tid] = (int32_t)source_row(p, p0 + (tid < valid ? tid : valid - 1));
-  __syncthreads();
+  const int first = ((int)blockIdx.x & 7) * per_xcd;
+  const int end = first + per_xcd < total ? first + per_xcd : total;
+  const int stride = (int)gridDim.x >> 3;
+  int v = first + ((int)blockIdx.x >> 3);
+  if (v >= end) return;
+  MxTile cur = mx_tile(tiles, real_m, n_tiles, v);
+  MxTile nxt = cur;
+  if (v + stride < end) nxt = mx_tile(tiles, real_m, n_tiles, v + stride);
 
   const uint32_t KC = (uint32_t)(p.K / 2), KS = (uint32_t)(p.K / 32);
-  const int nk = (int)(p.K / BK);
-  const int64_t NO = GLU ? p.N / 2 : p.N;               // output columns
-  constexpr int CW = GLU ? 32 : 64;                     // ... of a wave
-  const int64_t n0 = (int64_t)nt * 4 * CW;
-  // weight row of the tile's row r (wave r / 64, of which GLU: 32 gate, 32 up)
-  auto w_row = [&](int r) -> uint32_t {
-    int64_t n = n0 + (GLU ? (r >> 6) * 32 + (r & 31) : r);
-    n = n < NO ? n : NO - 1;
-    return (uint32_t)(GLU && (r & 32) ? n + NO : n);
-  };
-  const uint8_t* wc = p.w_codes + (int64_t)e * p.N * KC;
-  const uint8_t* wsc = p.w_scales + (int64_t)e * p.N * KS;
-  const __amdgpu_buffer_rsrc_t rs_a = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(p.a_codes), (short)0, (int)(uint32_t)(p.M_src * KC), kBufferRsrcWord3);
-  const __amdgpu_buffer_rsrc_t rs_w = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(wc), (short)0, (int)(uint32_t)(p.N * KC), kBufferRsrcWord3);
+  const int nd = (int)(p.K / 128);                      // dwords of a row's scales
+  constexpr bool kHalf = ND % 2 == 1;                   // the last step is of 128 columns
+  constexpr bool kOdd = ND == 1 || ND == 2;             // an odd number of steps
+  const int ns = (nd + 1) / 2, M_last = (int)p.M_src - 1;
+  const uint32_t NO = (uint32_t)(GLU ? p.N / 2 : p.N);  // output columns
+  constexpr uint32_t CW = GLU ? 32 : 64;                // ... of a wave
+  const __amdgpu_buffer_rsrc_t rs_a = mx_buffer(p.a_codes, (uint64_t)p.M_src * KC);
+  const __amdgpu_buffer_rsrc_t rs_as = mx_buffer(p.a_scales, (uint64_t)p.M_src * KS);
 
-  // one load instruction fills 16 rows of 64 bytes: lane l's 16 bytes land at
-  // row l / 4, place l % 4
-  const int lr = lane >> 2, piece = (lane & 3) ^ ((lr >> 2) & 3);
-  uint32_t off_a[2], off_w[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    off_a[i] = (uint32_t)rows_src[(2 * wave + i) * 16 + lr] * KC + 16u * piece;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) off_w[i] = w_row((4 * wave + i) * 16 + lr) * KC + 16u * piece;
-  auto issue_loads = [&](uint8_t* st, int kt) {
-    const uint32_t k0 = (uint32_t)kt * 64u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(st + (2 * wave + i) * 1024), 16, off_a[i],
-                                               k0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_w, lds_ptr(st + A_BYTES + (4 * wave + i) * 1024), 16,
-                                               off_w[i], k0, 0, 0);
-  };
-  // scales: weight rows 64 wave + 32 i + r32, activation rows 32 j + r32
-  uint32_t soff_w[2], soff_a[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) soff_w[i] = w_row(64 * wave + 32 * i + r32) * KS;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) soff_a[j] = (uint32_t)rows_src[32 * j + r32] * KS;
-  typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
-  typedef u32x3 u32x3a __attribute__((aligned(4)));
-  u32x3 sw[2], sa[4];
-  auto load_scales = [&](int kt, auto full_c) {          // of steps kt .. kt + 2
-    auto get = [&](const uint8_t* base, uint32_t off) -> u32x3 {
-      const uint8_t* src = base + off + 4u * (uint32_t)kt;
-      if (decltype(full_c)::value || kt + 3 <= nk) return *reinterpret_cast<const u32x3a*>(src);
-      u32x3 s = {0, 0, 0};
-      s.x = *reinterpret_cast<const uint32_t*>(src);
-      if (kt + 1 < nk) s.y = *reinterpret_cast<const uint32_t*>(src + 4);
-      return s;
+  // ---- loads.  A tile's loads go through these; they are set for the next
+  // tile when the current one's last are on their way.
+  __amdgpu_buffer_rsrc_t rs_w, rs_s;
+  uint32_t off_a[4], off_s[2];
+  uint32_t w_row0, w_row1;                              // the wave's first 32 weight rows, the other 32
+  // One load instruction fills 8 rows of 128 bytes: lane l's 16 bytes land at
+  // row l / 8, place l % 8.  (The lane is taken afresh each time, so that what
+  // follows from it is not kept in registers through the products.)
+  auto aim = [&](const MxTile& t, const int32_t* src) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    const uint32_t n0 = (uint32_t)t.nt * 4 * CW;
+    auto a_row = [&](int r) -> uint32_t {
+      const int s = p.a_rows ? src[r] : t.p0 + (r < t.valid ? r : t.valid - 1);
+      return (uint32_t)max(0, min(s, M_last));
     };
+    // (multiplied apart from the addition: a 64-bit multiply-add would hold a
+    // pair of registers for each offset)
+    auto times = [](uint32_t a, uint32_t b) {
+      uint32_t m = a * b;
+      asm volatile("" : "+v"(m));
+      return m;
+    };
+    rs_w = mx_buffer(p.w_codes + (int64_t)t.e * p.N * KC, (uint64_t)p.N * KC);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sw[i] = get(wsc, soff_w[i]);
+    for (int i = 0; i < 4; ++i) {
+      const int r = (4 * wave + i) * 8 + (lane >> 3);
+      off_a[i] = times(a_row(r), KC) + 16u * ((lane & 7) ^ ((r >> 1) & 7));
+    }
+    w_row0 = n0 + CW * wave;
+    w_row1 = GLU ? w_row0 + NO : w_row0 + 32;
+    // scales: wave 0 the activation rows', waves 1 and 2 the weight rows' (3:
+    // the same as 2, so that every wave has as many loads in flight); the
+    // tile's weight row r is wave r / 64's row r % 64
+    rs_s = wave == 0 ? rs_as : mx_buffer(p.w_scales + (int64_t)t.e * p.N * KS, (uint64_t)p.N * KS);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sa[j] = get(p.a_scales, soff_a[j]);
+    for (int i = 0; i < 2; ++i) {
+      const int r = (wave < 2 ? 0 : 128) + 64 * i + lane;
+      uint32_t n = n0 + (uint32_t)(GLU ? (r >> 6) * 32 + (r & 31) : r);
+      n = n < NO ? n : NO - 1;
+      off_s[i] = times(wave == 0 ? a_row(r) : GLU && (r & 32) ? n + NO : n, KS);
+    }
   };
-
-  f32x16_t acc[2][4];
+  // A last step of 128 columns has rows of 64 bytes: the lanes of the pieces 4
+  // to 7, the odd four of an even instruction, load 0 to 3 instead.
+  auto cut = [&](int kt, int i) -> uint32_t {
+    return kHalf && 2 * kt + 1 == nd && (((lane >> 2) ^ i) & 1) ? 64u : 0u;
+  };
+  auto issue_a = [&](uint8_t* st, int kt) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t off = off_a[i] - cut(kt, i);
+      const uint32_t k0 = 128u * (uint32_t)kt;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_a, lds_ptr(st + (4 * wave + i) * 1024), 16, off, k0, 0, 0);
+    }
+  };
+  // rows of the lanes of one instruction, and their places' pieces: of the even
+  // instructions and of the odd
+  const uint32_t w_lane = (uint32_t)(lane >> 3) * KC;
+  const uint32_t off_w0 = w_lane + 16u * ((lane & 7) ^ (lane >> 4));
+  const uint32_t off_w1 = w_lane + 16u * ((lane & 7) ^ (lane >> 4) ^ 4);
+  auto issue_w = [&](int kt) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < 8; ++i) {
+      // (rows past the last: the last 8, of which nothing is stored)
+      uint32_t r = (i < 4 ? w_row0 : w_row1) + 8u * (i & 3);
+      r = r < (uint32_t)p.N - 8u ? r : (uint32_t)p.N - 8u;
+      const uint32_t off = (i & 1 ? off_w1 : off_w0) - cut(kt, i);
+      const uint32_t k0 = r * KC + 128u * (uint32_t)kt;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_w, lds_ptr(sw + (8 * wave + i) * 1024), 16, off, k0, 0, 0);
+    }
+  };
+  // the scales of two steps (the last 16 bytes of a row, where fewer are left),
+  // row after row; of rows of fewer bytes dword after dword
+  auto issue_scales = [&](int kt) {
+    const int r0 = 128 * (wave < 2 ? wave : 2);
+    if (ND == 0 || nd >= 4) {
+      const uint32_t s0 = 8u * kt < KS - 16u ? 8u * kt : KS - 16u;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
+      for (int i = 0; i < 2; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_s, lds_ptr(ssc + (r0 + 64 * i) * 16), 16, off_s[i], s0,
+                                                 0, 0);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < nd; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs_s, lds_ptr(ssc + (384 * k + r0 + 64 * i) * 4), 4,
+                                                   off_s[i], 4u * k, 0, 0);
+    }
+  };
+  // a tile's row list, straight to LDS
+  auto issue_rows = [&](const MxTile& t, int32_t* dst) {
+    if (wave < 2) {
+      const int r = 64 * wave + lane;
+      const __amdgpu_buffer_rsrc_t rs = mx_buffer(p.a_rows + t.p0, 4ull * t.valid);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, lds_ptr(dst + 64 * wave), 4,
+                                               4u * (r < t.valid ? r : t.valid - 1), 0, 0, 0);
+    }
+  };
   // (one offset per read: the compiler follows short address chains only when
   // it decides which loads into LDS a read has to wait for)
-  const uint32_t place[2] = {(uint32_t)(r32 * 64 + (((2 * q) ^ ((r32 >> 2) & 3)) << 4)),
-                             (uint32_t)(r32 * 64 + (((2 * q + 1) ^ ((r32 >> 2) & 3)) << 4))};
-  const uint32_t w_place[2] = {place[0] + (uint32_t)(A_BYTES + 4096 * wave),
-                               place[1] + (uint32_t)(A_BYTES + 4096 * wave)};
   auto ld = [&](const uint8_t* st, uint32_t off) -> u32x4 {
     return *reinterpret_cast<const u32x4*>(st + off);
   };
+  auto ld_scale = [&](uint32_t off) -> uint32_t {
+    return *reinterpret_cast<const uint32_t*>(ssc + off);
+  };
 
-  auto run = [&](auto nv_c) {
-    constexpr int NV = decltype(nv_c)::value;
-    // FULL: the steps kt + 1 .. kt + 3 are there, and those whose scales are
-    // loaded here
-    auto step = [&](const uint8_t* st, uint8_t* next, int kt, auto sub_c, auto full_c) {
-      constexpr int SUB = decltype(sub_c)::value;
-      constexpr bool FULL = decltype(full_c)::value;
-      // all but the newest stage's loads are there; every wave is past the
-      // stage that is filled next
-      if (FULL || kt + 1 < nk) asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)" ::: "memory");
-      else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      uint32_t tw[2], ta[NV];
+  int buf = 0;
+  if (p.a_rows) {
+    issue_rows(cur, rows[0]);
+    mx_wait<0>();
+    mx_barrier();
+  }
+  aim(cur, rows[0]);
+  issue_scales(0);
+  issue_a(sa0, 0);
+  issue_w(0);
+
+  constexpr int kStores = GLU ? 8 : 16;                 // of a whole tile, per wave
+  int stores = 0;                                       // the last tile's
+  bool odd = false;                                     // the tile's first step is in sa1
+  for (;;) {
+    const bool more = v + stride < end;
+    if (more && p.a_rows) issue_rows(nxt, rows[buf ^ 1]);
+    MxTile nn = nxt;
+    if (v + 2 * stride < end) nn = mx_tile(tiles, real_m, n_tiles, v + 2 * stride);
+
+    // NV: blocks of 32 activation rows; x: the stage of the even steps
+    auto run = [&](auto nv_c, uint8_t* const x, uint8_t* const y) {
+      constexpr int NV = decltype(nv_c)::value;
+      f32x16_t acc[2][NV];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) tw[i] = sw[i][SUB] >> (16 * q);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) ta[j] = sa[j][SUB] >> (16 * q);
-      if (SUB == 2 && (FULL || kt + 1 < nk)) load_scales(kt + 1, full_c);
-      asm volatile("" ::: "memory");                     // (older than the stage's loads)
-      if (FULL || kt + 2 < nk) issue_loads(next, kt + 2);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 W[2], A[NV];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) W[i] = ld(st, w_place[s] + 2048u * i);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) A[j] = ld(st, place[s] + 2048u * j);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            acc[i][j] = s == 0 ? mfma32_mx4<0>(W[i], tw[i], A[j], ta[j], acc[i][j])
-                               : mfma32_mx4<1>(W[i], tw[i], A[j], ta[j], acc[i][j]);
-      }
-    };
-    using c0 = std::integral_constant<int, 0>;
-    using c1 = std::integral_constant<int, 1>;
-    using c2 = std::integral_constant<int, 2>;
-    using all = std::true_type;
-    using some = std::false_type;
-    load_scales(0, some{});
-    issue_loads(st0, 0);
-    if (nk > 1) issue_loads(st1, 1);
-    int kt = 0;
-    for (; kt + 5 < nk; kt += 3) {
-      step(st0, st2, kt, c0{}, all{});
-      step(st1, st0, kt + 1, c1{}, all{});
-      step(st2, st1, kt + 2, c2{}, all{});
-    }
-    for (; kt < nk; kt += 3) {
-      step(st0, st2, kt, c0{}, some{});
-      if (kt + 1 < nk) step(st1, st0, kt + 1, c1{}, some{});
-      if (kt + 2 < nk) step(st2, st1, kt + 2, c2{}, some{});
-    }
-    // lane (r, q) holds columns 8 g + 4 q .. + 3 of its row in registers 4 g ..
-    // 4 g + 3: one exchange between the lane halves makes 16-byte pieces
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+      uint32_t tw[2][2], ta[2][NV];                     // scales of a pair of steps
+      // One step, from stage st; the next one's activation rows go to `other`.
+      // U: the first or the second of a pair.  LAST: the tile's last, after
+      // which comes the next tile's first; HALF: of 128 columns.
+      auto step = [&](int kt, uint8_t* st, uint8_t* other, auto u_c, auto last_c, auto half_c) {
+        constexpr int U = decltype(u_c)::value;
+        constexpr bool LAST = decltype(last_c)::value, HALF = decltype(half_c)::value;
+        constexpr int S = HALF ? 2 : 4;
+        if (kt > 0 || ns == 1) mx_wait<0>();
+        else if (stores == kStores) mx_wait<kStores>();
+        else if (stores) mx_wait<kStores / 2>();
+        else mx_wait<0>();
+        mx_barrier();
+        if constexpr (U == 0) {
+          // dword 2 u + q of the step u of the pair (HALF: 2 u, and two of its
+          // bytes), behind those that a pair at the end of a row has before it
+          const int left = nd - 2 * kt;                 // dwords of the pair that are there
+          const bool wide = ND == 0 || nd >= 4;
+          const uint32_t per_row = wide ? 16 : 4, per_dword = wide ? 4 : 1536;
+          const uint32_t d0 = ND != 0 && wide && left < 4 ? (uint32_t)(4 - left) : 0u;
+          auto get = [&](int u, bool half) {
+            const uint32_t at = (d0 + 2u * u + (half ? 0u : (uint32_t)q)) * per_dword;
+            const int sh = half ? 16 * q : 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int row = 32 * j + r32;
-      uint16_t* dst = p.y + (p0 + row) * NO;
+            for (int i = 0; i < 2; ++i)
+              tw[u][i] = ld_scale((uint32_t)(BM + 64 * wave + 32 * i + r32) * per_row + at) >> sh;
 #pragma unroll
-      for (int i = 0; i < (GLU ? 1 : 2); ++i)
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          uint32_t u[4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int x = 4 * (g + h) + 2 * c;
-              u[2 * h + c] = GLU ? bf16x2_rne(silu_mul(acc[0][j][x], acc[1][j][x]),
-                                              silu_mul(acc[0][j][x + 1], acc[1][j][x + 1]))
-                                 : bf16x2_rne(acc[i][j][x], acc[i][j][x + 1]);
-            }
-          // lanes below 32 get all of columns 8 g .., the others of 8 (g + 1) ..
-          const auto x0 = __builtin_amdgcn_permlane32_swap(u[0], u[2], false, false);
-          const auto x1 = __builtin_amdgcn_permlane32_swap(u[1], u[3], false, false);
-          const int64_t n = n0 + CW * wave + 32 * i + 8 * (g + q);
-          if (row < valid && n < NO)
-            *reinterpret_cast<uint4*>(dst + n) = make_uint4(x0[0], x1[0], x0[1], x1[1]);
+            for (int j = 0; j < NV; ++j) ta[u][j] = ld_scale((uint32_t)(32 * j + r32) * per_row + at) >> sh;
+          };
+          get(0, ND == 1 && left == 1);
+          if (ND == 0 || left > 2) get(1, ND == 3 && left == 3);
         }
-    }
-  };
-  if (valid > 96) run(std::integral_constant<int, 4>{});
-  else if (valid > 64) run(std::integral_constant<int, 3>{});
-  else if (valid > 32) run(std::integral_constant<int, 2>{});
-  else run(std::integral_constant<int, 1>{});
+        uint32_t here = (uint32_t)(r32 * 128 + (((HALF ? 2 * q : 4 * q) ^ ((r32 >> 1) & 7)) << 4));
+        asm volatile("" : "+v"(here));                   // (its sums are not kept in registers)
+        u32x4 W[S][2], A[S][NV];
+        auto read_a = [&](int s) {
+#pragma unroll
+          for (int j = 0; j < NV; ++j) A[s][j] = ld(st, (here ^ (16u * s)) + 4096u * j);
+        };
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) W[s][i] = ld(sw, (here ^ (16u * s)) + (uint32_t)(8192 * wave) + 4096u * i);
+        read_a(0);
+        const bool ahead = !LAST || more;
+        if (LAST && more) aim(nxt, rows[buf ^ 1]);
+        if (ahead) issue_a(other, LAST ? 0 : kt + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if (s + 1 < S) read_a(s + 1);
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (s == 0) acc[i][j] = mfma32_mx4<0>(W[s][i], tw[U][i], A[s][j], ta[U][j], acc[i][j]);
+              if (s == 1) acc[i][j] = mfma32_mx4<1>(W[s][i], tw[U][i], A[s][j], ta[U][j], acc[i][j]);
+              if (s == 2) acc[i][j] = mfma32_mx4<2>(W[s][i], tw[U][i], A[s][j], ta[U][j], acc[i][j]);
+              if (s == 3) acc[i][j] = mfma32_mx4<3>(W[s][i], tw[U][i], A[s][j], ta[U][j], acc[i][j]);
+            }
+          __builtin_amdgcn_sched_barrier(0);
+          if (s == 0 && ahead) {
+            // the first products waited for the last of the weights' reads:
+            // their stage is free.  The scales' is one step later, or once every
+            // wave has read the tile's last.
+            issue_w(LAST ? 0 : kt + 1);
+            if (U == 1 || LAST) {
+              if (U == 0) mx_barrier();
+              issue_scales(LAST ? 0 : kt + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        // (the products belong here, not behind the next wait)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) asm volatile("" : "+v"(acc[i][j]));
+      };
+      using u0 = std::integral_constant<int, 0>;
+      using u1 = std::integral_constant<int, 1>;
+      using yes = std::true_type;
+      using no = std::false_type;
+      using half = std::integral_constant<bool, kHalf>;
+      int kt = 0;
+      for (; kt + 2 < ns; kt += 2) {
+        step(kt, x, y, u0{}, no{}, no{});
+        step(kt + 1, y, x, u1{}, no{}, no{});
+      }
+      if constexpr (kOdd) {
+        step(kt, x, y, u0{}, yes{}, half{});
+      } else {
+        step(kt, x, y, u0{}, no{}, no{});
+        step(kt + 1, y, x, u1{}, yes{}, half{});
+      }
+
+      // Rows of 128 bytes (GLU: 64) of the wave's columns, put together in 4 KB
+      // of the stage that nobody reads any more.  Rows past the tile's last lie
+      // past the buffer.
+      mx_wait<63>();
+      mx_barrier();
+      const __amdgpu_buffer_rsrc_t rs_y =
+          mx_buffer(p.y + (int64_t)cur.p0 * NO, (uint64_t)cur.valid * NO * 2);
+      const uint32_t n0 = (uint32_t)cur.nt * 4 * CW + CW * wave;
+      int l = threadIdx.x & 63;                          // (afresh, as in aim)
+      asm volatile("" : "+v"(l));
+      constexpr int LR = GLU ? 4 : 8;                   // lanes of a row of 16-byte pieces
+      auto put = [&](uint8_t* const own) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const int r = l & 31;
+#pragma unroll
+          for (int i = 0; i < (GLU ? 1 : 2); ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t u[2];
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int e = 4 * g + 2 * c;
+                u[c] = GLU ? bf16x2_rne(silu_mul(acc[0][j][e], acc[1][j][e]),
+                                        silu_mul(acc[0][j][e + 1], acc[1][j][e + 1]))
+                           : bf16x2_rne(acc[i][j][e], acc[i][j][e + 1]);
+              }
+              const int piece = GLU ? g ^ ((r >> 1) & 3) : (4 * i + g) ^ (r & 7);
+              *reinterpret_cast<uint2*>(own + (r * (16 * LR) + (piece << 4) + (l >> 5) * 8)) =
+                  make_uint2(u[0], u[1]);
+            }
+#pragma unroll
+          for (int t = 0; t < LR / 2; ++t) {
+            const int row = (64 / LR) * t + l / LR, c = l % LR;
+            const u32x4 o = *reinterpret_cast<const u32x4*>(
+                own + (row * (16 * LR) + ((GLU ? c ^ ((row >> 1) & 3) : c ^ (row & 7)) << 4)));
+            const uint32_t n = n0 + 8 * c;
+            __builtin_amdgcn_raw_buffer_store_b128(
+                o, rs_y, n < NO ? ((uint32_t)(32 * j + row) * NO + n) * 2u : 0xFFFFFFF0u, 0, 0);
+          }
+        }
+      };
+      put((kOdd ? x : y) + 4096 * wave);
+      stores = NV * (kStores / 4);
+    };
+    using n4 = std::integral_constant<int, 4>;
+    using n2 = std::integral_constant<int, 2>;
+    auto tile = [&](uint8_t* const x, uint8_t* const y) {
+      if (cur.valid > 64) run(n4{}, x, y);
+      else run(n2{}, x, y);
+    };
+    if (kOdd && odd) tile(sa1, sa0);
+    else tile(sa0, sa1);
+    if (!more) return;
+    v += stride;
+    cur = nxt;
+    nxt = nn;
+    buf ^= 1;
+    odd = !odd;
+  }
 }
 
 }  // namespace nvfp4
@@ -421,6 +593,17 @@ using namespace nvfp4;
 // row tiles of 128 that the experts' rows can make
 static int64_t mx_row_tiles(int64_t E, int64_t M_total) {
   return (M_total + mxb::BM - 1) / mxb::BM + E;
+}
+
+template <bool GLU>
+static void mx_launch_big(unsigned nb, hipStream_t s, const MxGemmArgs& p, const int4* tiles,
+                          const int32_t* count, int n_tiles) {
+  switch ((p.K / 128) % 4) {
+    case 0: k_mx_big<GLU, 0><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
+    case 1: k_mx_big<GLU, 1><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
+    case 2: k_mx_big<GLU, 2><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
+    default: k_mx_big<GLU, 3><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
+  }
 }
 
 static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uint8_t* a_scales,
@@ -456,16 +639,18 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
   const int64_t NO = glu ? N / 2 : N;
   if (M_total > 32 * E) {
     const int64_t n_tiles = (N + mxb::BN - 1) / mxb::BN, m_tiles = mx_row_tiles(E, M_total);
-    NV_REQUIRE(m_tiles * n_tiles < (1 << 24), NVFP4_ERR_UNSUPPORTED, "%s: too many tiles", name);
+    NV_REQUIRE(m_tiles * n_tiles < (1 << 28), NVFP4_ERR_UNSUPPORTED, "%s: too many tiles", name);
     int32_t* count = static_cast<int32_t*>(ws);
     int4* tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + 256);
-    const unsigned nb = (unsigned)((m_tiles * n_tiles + 7) / 8 * 8);
+    // two workgroups per CU, a multiple of the XCDs
+    int64_t nb = (m_tiles * n_tiles + 7) / 8 * 8;
+    if (nb > 2 * num_cus()) nb = (2 * num_cus() + 7) / 8 * 8;
     const int64_t tb = (m_tiles + 1023) / 1024;
     k_mx_tiles<<<(unsigned)(tb < 256 ? tb : 256), 1024, 0, s>>>(p, tiles, count);
     if (glu)
-      k_mx_big<true><<<nb, 256, 0, s>>>(p, tiles, count, (int)n_tiles);
+      mx_launch_big<true>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
     else
-      k_mx_big<false><<<nb, 256, 0, s>>>(p, tiles, count, (int)n_tiles);
+      mx_launch_big<false>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
     return check_launch(name);
   }
   const int64_t avg = (M_total + E - 1) / E;
