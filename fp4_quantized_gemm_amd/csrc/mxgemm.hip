@@ -167,7 +167,7 @@ constexpr int A_BYTES = BM * 128, W_BYTES = BN * 128, SCALES = (BM + BN) * 16;
 }  // namespace mxb
 
 // The row tiles of all experts, in order: tiles[t] = {expert, first row, rows,
-// 0}, and their number.  Every workgroup sums the experts' tiles for itself and
+// 0}, their number in n_tiles[0], and 0 in the eight behind it.  Every workgroup sums the experts' tiles for itself and
 // writes a part of the list.
 __global__ void __launch_bounds__(1024)
 k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
@@ -204,7 +204,7 @@ k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles
     const int64_t p0 = lo + (int64_t)(t - prefix[lo_e]) * mxb::BM;
     tiles[t] = make_int4(lo_e, (int)p0, (int)(hi - p0 < mxb::BM ? hi - p0 : mxb::BM), 0);
   }
-  if (blockIdx.x == 0 && tid == 0) *n_tiles = total;
+  if (blockIdx.x == 0 && tid < 9) n_tiles[tid] = tid == 0 ? total : 0;
 }
 
 // D += 2^(sa - 127 + sb - 127) A B over 64 k: lane (r = l % 32, q = l / 32)
@@ -252,21 +252,22 @@ __device__ __forceinline__ MxTile mx_tile(const int4* __restrict__ tiles, int re
 // ND: K / 128 modulo 4, so what the last steps are
 template <bool GLU, int ND>
 __global__ void __launch_bounds__(256, 2)
-k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict__ n_row_tiles,
+k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_row_tiles,
          int n_tiles) {
   using namespace mxb;
   // separate objects, each access naming its own: the compiler then does not
   // wait for loads into the others
   __shared__ __attribute__((aligned(16))) uint8_t sa0[A_BYTES], sa1[A_BYTES], sw[W_BYTES], ssc[SCALES];
-  __shared__ int32_t rows[2][BM];
+  __shared__ int32_t rows[2][BM], next_v;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 5, r32 = lane & 31;
 
   // each XCD (workgroup b runs on XCD b % 8) takes a contiguous range of the
-  // tiles, so its L2 holds an expert's weights; its workgroups every
-  // (gridDim / 8)-th of them
+  // tiles, so its L2 holds an expert's weights; its workgroups start with one
+  // each and a second, then take the next that nobody has (which workgroup
+  // computes a tile does not show in it)
   const int real_m = *n_row_tiles;
   const int total = real_m * n_tiles;
   const int per_xcd = (total + 7) / 8;
@@ -276,8 +277,8 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict
   int v = first + ((int)blockIdx.x >> 3);
   if (v >= end) return;
   MxTile cur = mx_tile(tiles, real_m, n_tiles, v);
-  MxTile nxt = cur;
-  if (v + stride < end) nxt = mx_tile(tiles, real_m, n_tiles, v + stride);
+  v += stride;                                          // the next one
+  int32_t* const tickets = n_row_tiles + 1 + (blockIdx.x & 7);
 
   const uint32_t KC = (uint32_t)(p.K / 2), KS = (uint32_t)(p.K / 32);
   const int nd = (int)(p.K / 128);                      // dwords of a row's scales
@@ -413,10 +414,14 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict
   int stores = 0;                                       // the last tile's
   bool odd = false;                                     // the tile's first step is in sa1
   for (;;) {
-    const bool more = v + stride < end;
-    if (more && p.a_rows) issue_rows(nxt, rows[buf ^ 1]);
-    MxTile nn = nxt;
-    if (v + 2 * stride < end) nn = mx_tile(tiles, real_m, n_tiles, v + 2 * stride);
+    const bool more = v < end;
+    MxTile nxt = cur;
+    int ticket = 0;
+    if (more) {
+      nxt = mx_tile(tiles, real_m, n_tiles, v);
+      if (p.a_rows) issue_rows(nxt, rows[buf ^ 1]);
+      if (tid == 0) ticket = atomicAdd(tickets, 1);
+    }
 
     // NV: blocks of 32 activation rows; x: the stage of the even steps
     auto run = [&](auto nv_c, uint8_t* const x, uint8_t* const y) {
@@ -473,7 +478,10 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict
           for (int i = 0; i < 2; ++i) W[s][i] = ld(sw, (here ^ (16u * s)) + (uint32_t)(8192 * wave) + 4096u * i);
         read_a(0);
         const bool ahead = !LAST || more;
-        if (LAST && more) aim(nxt, rows[buf ^ 1]);
+        if (LAST && more) {
+          aim(nxt, rows[buf ^ 1]);
+          if (tid == 0) next_v = first + 2 * stride + ticket;
+        }
         if (ahead) issue_a(other, LAST ? 0 : kt + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -551,18 +559,22 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict
                                         silu_mul(acc[0][j][e + 1], acc[1][j][e + 1]))
                            : bf16x2_rne(acc[i][j][e], acc[i][j][e + 1]);
               }
-              const int piece = GLU ? g ^ ((r >> 1) & 3) : (4 * i + g) ^ (r & 7);
-              *reinterpret_cast<uint2*>(own + (r * (16 * LR) + (piece << 4) + (l >> 5) * 8)) =
+              // (32 rows' 8 bytes cover all banks once)
+              const int piece = GLU ? g ^ ((r >> 2) & 3) : (4 * i + g) ^ ((r >> 1) & 7);
+              const int half = (l >> 5) ^ (r >> 4);
+              *reinterpret_cast<uint2*>(own + (r * (16 * LR) + (piece << 4) + half * 8)) =
                   make_uint2(u[0], u[1]);
             }
 #pragma unroll
           for (int t = 0; t < LR / 2; ++t) {
             const int row = (64 / LR) * t + l / LR, c = l % LR;
-            const u32x4 o = *reinterpret_cast<const u32x4*>(
-                own + (row * (16 * LR) + ((GLU ? c ^ ((row >> 1) & 3) : c ^ (row & 7)) << 4)));
+            const u32x4 h = *reinterpret_cast<const u32x4*>(
+                own + (row * (16 * LR) + ((GLU ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7)) << 4)));
+            // (rows 16 .. 31, the second half of the reads, have their halves swapped)
+            const u32x4 o = t < LR / 4 ? h : u32x4{h.z, h.w, h.x, h.y};
             const uint32_t n = n0 + 8 * c;
             __builtin_amdgcn_raw_buffer_store_b128(
-                o, rs_y, n < NO ? ((uint32_t)(32 * j + row) * NO + n) * 2u : 0xFFFFFFF0u, 0, 0);
+                o, rs_y, n < NO ? ((uint32_t)(32 * j + row) * NO + n) * 2u : 0xFFFFFFF0u, 0, 2);
           }
         }
       };
@@ -578,9 +590,8 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, const int32_t* __restrict
     if (kOdd && odd) tile(sa1, sa0);
     else tile(sa0, sa1);
     if (!more) return;
-    v += stride;
+    v = __builtin_amdgcn_readfirstlane(next_v);
     cur = nxt;
-    nxt = nn;
     buf ^= 1;
     odd = !odd;
   }
@@ -597,7 +608,7 @@ static int64_t mx_row_tiles(int64_t E, int64_t M_total) {
 
 template <bool GLU>
 static void mx_launch_big(unsigned nb, hipStream_t s, const MxGemmArgs& p, const int4* tiles,
-                          const int32_t* count, int n_tiles) {
+                          int32_t* count, int n_tiles) {
   switch ((p.K / 128) % 4) {
     case 0: k_mx_big<GLU, 0><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
     case 1: k_mx_big<GLU, 1><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
