@@ -53,27 +53,48 @@ __device__ __forceinline__ int64_t source_row(const MxGemmArgs& p, int64_t row) 
   return t < 0 ? 0 : (t >= p.M_src ? p.M_src - 1 : t);
 }
 
-// Weight streaming, without LDS: each wave owns R groups of 16 weight rows
-// and multiplies all of K with TT tiles of 16 activation rows, operands
-// straight from memory to registers.  K advances in chunks of 512: lane (r,
-// q) takes the 16-byte pieces 4 s + q, s = 0 .. 3, of its row's 256 bytes (64
-// contiguous bytes of a row per load), and the chunk's 16 scale bytes, of
-// which byte q of dword s belongs to piece s.
-// GLU: half of the groups are gate columns, the other half the same up ones.
+// ------------------------------------------------------------------------
+// Weight streaming, without LDS, for few rows per expert: a workgroup owns 64 R
+// weight rows, a wave R groups of 16 of them, and multiplies all of K with one
+// or two tiles of 16 activation rows, operands straight from memory to
+// registers.  K advances in chunks of 512, the next one under way while one is
+// multiplied.  Lane (r, q) takes the 16-byte pieces 4 s + q, s = 0 .. 3, of its
+// row's 256 bytes, and the chunk's 16 scale bytes, of which byte q of dword s
+// belongs to piece s.
+// GLU: half of a wave's groups are gate columns, the other half the same up
+// ones.
+//
+// Bound by the weights' bytes: 2048 rows for 128 experts of 4096x1536, 99 us =
+// 4.4 TB/s with R = 2 (R = 1: 115, R = 4: 105; nontemporal loads 110, a line
+// being read in two halves; two, four and eight such blocks per workgroup, the
+// next one's first chunk under way at the end of one, 3, 7 and 9% slower).
+// Where that gives fewer than two workgroups per CU, R = 1: one token's 8
+// experts 13.5 us against 14.3, 64 rows of one 512x512 12.8 against 14.6.
+// ------------------------------------------------------------------------
+template <int R, int TT>
+struct MxChunk {
+  u32x4 w[R][4], sw[R], a[TT][4], sa[TT];
+};
+
 template <int R, int TT, bool GLU>
-__global__ void __launch_bounds__(256, 2)
-k_mx_few(MxGemmArgs p) {
+__device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t p0, int64_t hi) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
-  const int e = blockIdx.y;
-  int64_t lo, hi;
-  expert_rows(p, e, lo, hi);
   constexpr int RO = GLU ? R / 2 : R;                  // output groups
   const int64_t NO = GLU ? p.N / 2 : p.N;              // output columns
-  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16 * RO;
-  if (n0 >= NO) return;
   const int64_t KC = p.K / 2, KS = p.K / 32;
+  const int nd = (int)(p.K / 128), nch = (nd + 3) / 4;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16 * RO;
+  const uint8_t* ac[TT];
+  const uint8_t* asc[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t row = p0 + 16 * t + r16;
+    const int64_t src = source_row(p, row < hi ? row : hi - 1);
+    ac[t] = p.a_codes + src * KC + 16 * q;
+    asc[t] = p.a_scales + src * KS;
+  }
   const uint8_t* wc[R];
   const uint8_t* wsc[R];
 #pragma unroll
@@ -84,57 +105,85 @@ k_mx_few(MxGemmArgs p) {
     wc[g] = p.w_codes + ((int64_t)e * p.N + n) * KC + 16 * q;
     wsc[g] = p.w_scales + ((int64_t)e * p.N + n) * KS;
   }
-  for (int64_t p0 = lo + (int64_t)blockIdx.z * 16 * TT; p0 < hi; p0 += (int64_t)gridDim.z * 16 * TT) {
-    const uint8_t* ac[TT];
-    const uint8_t* asc[TT];
+  typedef u32x4 u32x4a __attribute__((aligned(4)));     // (rows of scales are whole dwords)
+  using Chunk = MxChunk<R, TT>;
+  auto load = [&](Chunk& k, int c) {
+    const int m = nd - 4 * c;                           // pieces that are there, if fewer than 4
+    const int64_t kc = 256 * c, ks = 16 * c;
+    auto row = [&](u32x4* pieces, u32x4& scales, const uint8_t* codes, const uint8_t* bytes) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int64_t row = p0 + 16 * t + r16;
-      const int64_t src = source_row(p, row < hi ? row : hi - 1);
-      ac[t] = p.a_codes + src * KC + 16 * q;
-      asc[t] = p.a_scales + src * KS;
-    }
-    f32x4_t acc[R][TT];
+      for (int s = 0; s < 4; ++s)
+        if (s < m) pieces[s] = *reinterpret_cast<const u32x4*>(codes + kc + 64 * s);
+      if (m >= 4) {
+        scales = *reinterpret_cast<const u32x4a*>(bytes + ks);
+      } else {
 #pragma unroll
-    for (int g = 0; g < R; ++g)
-#pragma unroll
-      for (int t = 0; t < TT; ++t) acc[g][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int64_t k = 0; k < p.K; k += 128) {
-      const uint32_t sh = 8 * q;
-      u32x4 a[TT];
-      uint32_t sa[TT];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        a[t] = *reinterpret_cast<const u32x4*>(ac[t] + k / 2);
-        sa[t] = *reinterpret_cast<const uint32_t*>(asc[t] + k / 32) >> sh;
+        for (int s = 0; s < 3; ++s)
+          if (s < m) scales[s] = reinterpret_cast<const uint32_t*>(bytes + ks)[s];
       }
+    };
 #pragma unroll
-      for (int g = 0; g < R; ++g) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(wc[g] + k / 2);
-        const uint32_t sw = *reinterpret_cast<const uint32_t*>(wsc[g] + k / 32) >> sh;
+    for (int g = 0; g < R; ++g) row(k.w[g], k.sw[g], wc[g], wsc[g]);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[g][t] = mfma16_mx4(w, sw, a[t], sa[t], acc[g][t]);
+    for (int t = 0; t < TT; ++t) row(k.a[t], k.sa[t], ac[t], asc[t]);
+  };
+  f32x4_t acc[R][TT];
+#pragma unroll
+  for (int g = 0; g < R; ++g)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[g][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Chunk& k, int c) {
+    const int m = nd - 4 * c;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (s < m) {
+#pragma unroll
+        for (int g = 0; g < R; ++g)
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            acc[g][t] = mfma16_mx4(k.w[g][s], k.sw[g][s] >> (8 * q), k.a[t][s], k.sa[t][s] >> (8 * q),
+                                   acc[g][t]);
       }
-    }
-    // lane (r, q): columns n0 + 16 g + 4 q .. + 3 of row p0 + 16 t + r
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int64_t row = p0 + 16 * t + r16;
-      if (row >= hi) continue;
-#pragma unroll
-      for (int g = 0; g < RO; ++g) {
-        const int64_t n = n0 + 16 * g + 4 * q;
-        if (n >= NO) continue;
-        f32x4_t v = acc[g][t];
-        if constexpr (GLU) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[g + RO][t][i]);
-        }
-        *reinterpret_cast<uint2*>(p.y + row * NO + n) =
-            make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
-      }
+  };
+  Chunk k0, k1;
+  load(k0, 0);
+  for (int c = 0; c < nch; c += 2) {
+    if (c + 1 < nch) load(k1, c + 1);
+    multiply(k0, c);
+    if (c + 1 < nch) {
+      if (c + 2 < nch) load(k0, c + 2);
+      multiply(k1, c + 1);
     }
   }
+  // lane (r, q): columns n0 + 16 g + 4 q .. + 3 of row p0 + 16 t + r
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int64_t row = p0 + 16 * t + r16;
+    if (row >= hi) continue;
+#pragma unroll
+    for (int g = 0; g < RO; ++g) {
+      const int64_t n = n0 + 16 * g + 4 * q;
+      if (n >= NO) continue;
+      f32x4_t v = acc[g][t];
+      if constexpr (GLU) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[g + RO][t][i]);
+      }
+      *reinterpret_cast<uint2*>(p.y + row * NO + n) =
+          make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+    }
+  }
+}
+
+template <int R, bool GLU>
+__global__ void __launch_bounds__(256, 2)
+k_mx_few(MxGemmArgs p) {
+  const int e = blockIdx.y;
+  int64_t lo, hi;
+  expert_rows(p, e, lo, hi);
+  int64_t p0 = lo + (int64_t)blockIdx.z * 32;
+  for (; p0 + 16 < hi; p0 += (int64_t)gridDim.z * 32) mx_few_tile<R, 2, GLU>(p, e, p0, hi);
+  if (p0 < hi) mx_few_tile<R, 1, GLU>(p, e, p0, hi);
 }
 
 // ------------------------------------------------------------------------
@@ -667,11 +716,17 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
   const int64_t avg = (M_total + E - 1) / E;
   int64_t z = (avg + 31) / 32;
   if (z > 1024) z = 1024;
-  const dim3 grid((unsigned)((NO + (glu ? 63 : 127)) / (glu ? 64 : 128)), (unsigned)E, (unsigned)z);
+  // R = 2 where the experts that can have rows make two workgroups per CU
+  const int64_t active = M_total < E ? M_total : E;
+  const bool wide = (NO + 127) / 128 * active >= 2 * num_cus();
+  const int per = wide && !glu ? 128 : 64;
+  const dim3 grid((unsigned)((NO + per - 1) / per), (unsigned)E, (unsigned)z);
   if (glu)
-    k_mx_few<2, 2, true><<<grid, 256, 0, s>>>(p);
+    k_mx_few<2, true><<<grid, 256, 0, s>>>(p);
+  else if (wide)
+    k_mx_few<2, false><<<grid, 256, 0, s>>>(p);
   else
-    k_mx_few<2, 2, false><<<grid, 256, 0, s>>>(p);
+    k_mx_few<1, false><<<grid, 256, 0, s>>>(p);
   return check_launch(name);
 }
 
