@@ -811,15 +811,27 @@ def mxfp4_restore(codes, scales, out=None):
 def _mxfp4_gemm(name, a_codes, a_scales, a_rows, w_codes, w_scales, expert_offsets, M_total, out,
                 glu):
     dev = _device_of(a_codes, "a_codes")
-    wp = _arg(w_codes, torch.uint8, "w_codes", dev, (None, None, None))
-    E, N, half = w_codes.shape
-    K = 2 * half
-    wsp = _arg(w_scales, torch.uint8, "w_scales", dev, (E, N, K // 32))
-    ap = _arg(a_codes, torch.uint8, "a_codes", dev, (None, half))
-    M_src = a_codes.shape[0]
-    asp = _arg(a_scales, torch.uint8, "a_scales", dev, (M_src, K // 32))
+    u8 = torch.uint8
+    E, N, half = w_codes.shape if getattr(w_codes, "ndim", 0) == 3 else (None, None, None)
+    M_src, K = a_codes.shape[0] if a_codes.ndim else 0, 2 * (half or 0)
+    # one comparison for all of it; _arg names what is wrong
+    try:
+        fits = (a_codes.shape == (M_src, half) and a_scales.shape == (M_src, K // 32) and
+                w_scales.shape == (E, N, K // 32) and expert_offsets.shape == (E + 1,) and
+                a_codes.dtype is u8 and a_scales.dtype is u8 and w_codes.dtype is u8 and
+                w_scales.dtype is u8 and expert_offsets.dtype is torch.int32 and
+                a_scales.device == w_codes.device == w_scales.device == expert_offsets.device == dev and
+                a_codes.is_contiguous() and a_scales.is_contiguous() and w_codes.is_contiguous() and
+                w_scales.is_contiguous() and expert_offsets.is_contiguous())
+    except (AttributeError, TypeError):
+        fits = False
+    if not fits:
+        _arg(w_codes, u8, "w_codes", dev, (None, None, None))
+        _arg(w_scales, u8, "w_scales", dev, (E, N, K // 32))
+        _arg(a_codes, u8, "a_codes", dev, (None, half))
+        _arg(a_scales, u8, "a_scales", dev, (M_src, K // 32))
+        _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
     rp = _arg(a_rows, torch.int32, "a_rows", dev, (None,), optional=True)
-    op = _arg(expert_offsets, torch.int32, "expert_offsets", dev, (E + 1,))
     M_total = _m_total(M_total, M_src, a_rows)
     cols = N // 2 if glu else N
     yp = _arg(out, torch.bfloat16, "out", dev, (M_total, cols), optional=True)
@@ -827,8 +839,9 @@ def _mxfp4_gemm(name, a_codes, a_scales, a_rows, w_codes, w_scales, expert_offse
         out = torch.empty((M_total, cols), dtype=torch.bfloat16, device=dev)
         yp = out.data_ptr()
     nb = (_lib or _load()).grouped_mxfp4_gemm_workspace_size(E, M_total, N, K)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-    _call(name, dev, ap, asp, rp, M_src, wp, wsp, op, E, M_total, N, K, yp, ws.data_ptr(), nb)
+    ws = torch.empty(nb, dtype=u8, device=dev)
+    _call(name, dev, a_codes.data_ptr(), a_scales.data_ptr(), rp, M_src, w_codes.data_ptr(),
+          w_scales.data_ptr(), expert_offsets.data_ptr(), E, M_total, N, K, yp, ws.data_ptr(), nb)
     return out
 
 

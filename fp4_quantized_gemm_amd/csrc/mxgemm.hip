@@ -54,38 +54,37 @@ __device__ __forceinline__ int64_t source_row(const MxGemmArgs& p, int64_t row) 
 }
 
 // ------------------------------------------------------------------------
-// Weight streaming, without LDS, for few rows per expert: a workgroup owns 64 R
-// weight rows, a wave R groups of 16 of them, and multiplies all of K with one
-// or two tiles of 16 activation rows, operands straight from memory to
-// registers.  K advances in chunks of 512, the next one under way while one is
-// multiplied.  Lane (r, q) takes the 16-byte pieces 4 s + q, s = 0 .. 3, of its
-// row's 256 bytes, and the chunk's 16 scale bytes, of which byte q of dword s
-// belongs to piece s.
-// GLU: half of a wave's groups are gate columns, the other half the same up
-// ones.
+// Small products, without LDS: a wave owns 16 weight rows (GLU: 16 gate rows and
+// the same 16 up rows) and multiplies all of K with one or two tiles of 16
+// activation rows, operands straight from memory to registers.  K advances in
+// chunks of 512, the next one under way while one is multiplied.  Lane (r, q)
+// takes the 16-byte pieces 4 s + q, s = 0 .. 3, of its row's 256 bytes, and the
+// chunk's 16 scale bytes, of which byte q of dword s belongs to piece s.
 //
-// Bound by the weights' bytes: 2048 rows for 128 experts of 4096x1536, 99 us =
-// 4.4 TB/s with R = 2 (R = 1: 115, R = 4: 105; nontemporal loads 110, a line
-// being read in two halves; two, four and eight such blocks per workgroup, the
-// next one's first chunk under way at the end of one, 3, 7 and 9% slower).
-// Where that gives fewer than two workgroups per CU, R = 1: one token's 8
-// experts 13.5 us against 14.3, 64 rows of one 512x512 12.8 against 14.6.
+// Bound by latency: one launch and a few round trips.  It is taken where all
+// experts' tiles of 16 rows times 64 columns are at most 512: one token's 8
+// experts of 4096x1536 (512 tiles) 11.4 us, 16 rows for each of 8 of them 12.8
+// against 15.5 with the large tiles (two launches), 64 rows for each of 4 of
+// 1536x2048 (384) 13.5 against 15.8; beyond, 48 rows for each of 8 of 1536x2048
+// (576) 15.7 against 15.7, 128 rows for each of 4 (768) 19.9 against 16.2, 16
+// rows for each of 128 58 against 49.
 // ------------------------------------------------------------------------
+// R: groups of 16 weight rows, TT: tiles of activation rows
 template <int R, int TT>
 struct MxChunk {
   u32x4 w[R][4], sw[R], a[TT][4], sa[TT];
 };
 
-template <int R, int TT, bool GLU>
+template <int TT, bool GLU>
 __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t p0, int64_t hi) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q = lane >> 4;
-  constexpr int RO = GLU ? R / 2 : R;                  // output groups
+  constexpr int R = GLU ? 2 : 1;
   const int64_t NO = GLU ? p.N / 2 : p.N;              // output columns
   const int64_t KC = p.K / 2, KS = p.K / 32;
   const int nd = (int)(p.K / 128), nch = (nd + 3) / 4;
-  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16 * RO;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
   const uint8_t* ac[TT];
   const uint8_t* asc[TT];
 #pragma unroll
@@ -99,9 +98,9 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
   const uint8_t* wsc[R];
 #pragma unroll
   for (int g = 0; g < R; ++g) {
-    int64_t n = n0 + 16 * (g % RO) + r16;
+    int64_t n = n0 + r16;
     n = n < NO ? n : NO - 1;
-    if (GLU && g >= RO) n += NO;
+    if (g == 1) n += NO;
     wc[g] = p.w_codes + ((int64_t)e * p.N + n) * KC + 16 * q;
     wsc[g] = p.w_scales + ((int64_t)e * p.N + n) * KS;
   }
@@ -155,35 +154,30 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
       multiply(k1, c + 1);
     }
   }
-  // lane (r, q): columns n0 + 16 g + 4 q .. + 3 of row p0 + 16 t + r
+  // lane (r, q): columns n0 + 4 q .. + 3 of row p0 + 16 t + r
+  const int64_t n = n0 + 4 * q;
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int64_t row = p0 + 16 * t + r16;
-    if (row >= hi) continue;
+    if (row >= hi || n >= NO) continue;
+    f32x4_t v = acc[0][t];
+    if constexpr (GLU) {
 #pragma unroll
-    for (int g = 0; g < RO; ++g) {
-      const int64_t n = n0 + 16 * g + 4 * q;
-      if (n >= NO) continue;
-      f32x4_t v = acc[g][t];
-      if constexpr (GLU) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[g + RO][t][i]);
-      }
-      *reinterpret_cast<uint2*>(p.y + row * NO + n) =
-          make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+      for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[1][t][i]);
     }
+    *reinterpret_cast<uint2*>(p.y + row * NO + n) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
   }
 }
 
-template <int R, bool GLU>
+template <bool GLU>
 __global__ void __launch_bounds__(256, 2)
 k_mx_few(MxGemmArgs p) {
   const int e = blockIdx.y;
   int64_t lo, hi;
   expert_rows(p, e, lo, hi);
   int64_t p0 = lo + (int64_t)blockIdx.z * 32;
-  for (; p0 + 16 < hi; p0 += (int64_t)gridDim.z * 32) mx_few_tile<R, 2, GLU>(p, e, p0, hi);
-  if (p0 < hi) mx_few_tile<R, 1, GLU>(p, e, p0, hi);
+  for (; p0 + 16 < hi; p0 += (int64_t)gridDim.z * 32) mx_few_tile<2, GLU>(p, e, p0, hi);
+  if (p0 < hi) mx_few_tile<1, GLU>(p, e, p0, hi);
 }
 
 // ------------------------------------------------------------------------
@@ -697,7 +691,10 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
                static_cast<uint16_t*>(y), M_src, M_total, N, K, (int)E};
   hipStream_t s = as_stream(stream);
   const int64_t NO = glu ? N / 2 : N;
-  if (M_total > 32 * E) {
+  // small: tiles of 16 rows of the experts that can have rows, times 64 columns
+  const int64_t blocks = (NO + 63) / 64, tiles16 = (M_total + 15) / 16;
+  const int64_t active = M_total < E ? M_total : E;
+  if (blocks * (tiles16 > active ? tiles16 : active) > 512) {
     const int64_t n_tiles = (N + mxb::BN - 1) / mxb::BN, m_tiles = mx_row_tiles(E, M_total);
     NV_REQUIRE(m_tiles * n_tiles < (1 << 28), NVFP4_ERR_UNSUPPORTED, "%s: too many tiles", name);
     int32_t* count = static_cast<int32_t*>(ws);
@@ -713,20 +710,12 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
       mx_launch_big<false>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
     return check_launch(name);
   }
-  const int64_t avg = (M_total + E - 1) / E;
-  int64_t z = (avg + 31) / 32;
-  if (z > 1024) z = 1024;
-  // R = 2 where the experts that can have rows make two workgroups per CU
-  const int64_t active = M_total < E ? M_total : E;
-  const bool wide = (NO + 127) / 128 * active >= 2 * num_cus();
-  const int per = wide && !glu ? 128 : 64;
-  const dim3 grid((unsigned)((NO + per - 1) / per), (unsigned)E, (unsigned)z);
+  const int64_t z = ((M_total + E - 1) / E + 31) / 32;  // (at most 1024: 512 tiles of 16 rows)
+  const dim3 grid((unsigned)blocks, (unsigned)E, (unsigned)z);
   if (glu)
-    k_mx_few<2, true><<<grid, 256, 0, s>>>(p);
-  else if (wide)
-    k_mx_few<2, false><<<grid, 256, 0, s>>>(p);
+    k_mx_few<true><<<grid, 256, 0, s>>>(p);
   else
-    k_mx_few<1, false><<<grid, 256, 0, s>>>(p);
+    k_mx_few<false><<<grid, 256, 0, s>>>(p);
   return check_launch(name);
 }
 
