@@ -56,64 +56,99 @@ k_combine_backward(const uint16_t* __restrict__ d_out, const uint16_t* __restric
   }
 }
 
-// A wave takes `per` consecutive tokens; lane l holds the experts l, l + 64,
+// A wave takes `per` consecutive tokens, as many at once as have their slots in
+// 64 lanes (a token's slots are 2^sh >= tk neighbours, 64 >> sh tokens), so that
+// one round trip brings the ids and weights of them all; the next ones' are
+// under way while these rows are written.  Lane l holds the experts l, l + 64,
 // ... of a row, finds its chosen ones by comparing with the row's ids, and
-// writes whole rows.  BIAS: the workgroup's sum of its rows goes to part.
+// writes whole rows.  An expert chosen twice by a token gets both gradients.
+// BIAS: the workgroup's sum of its rows goes to part; a wave adds up at most 64
+// rows in float32 and these sums in float64, as the terms of either sign cancel.
 template <int KPER, bool BIAS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(512)
 k_route_backward(const int32_t* __restrict__ ids, const float* __restrict__ w,
-                 const float* __restrict__ dw, int64_t T, int E, int tk, int per,
+                 const float* __restrict__ dw, int64_t T, int E, int tk, int sh, int per,
                  float* __restrict__ d_logits, float* __restrict__ part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t0 = (blockIdx.x * 4LL + wave) * per;
-  float sum[KPER];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (blockIdx.x * 8LL + wave) * per;
+  const int64_t t1 = t0 + per < T ? t0 + per : T;
+  const int at_once = 64 >> sh, j_own = lane & ((1 << sh) - 1);
+  double total[KPER];
 #pragma unroll
-  for (int i = 0; i < KPER; ++i) sum[i] = 0.0f;
-  for (int64_t t = t0; t < t0 + per && t < T; ++t) {
-    const bool in = lane < tk;
-    const int id = in ? ids[t * tk + lane] : -1;
-    const float wj = in ? w[t * tk + lane] : 0.0f, dj = in ? dw[t * tk + lane] : 0.0f;
+  for (int i = 0; i < KPER; ++i) total[i] = 0.0;
+  int id = -1;
+  float wj = 0.0f, dj = 0.0f;
+  auto fetch = [&](int64_t t) {
+    const int64_t own = t + (lane >> sh);
+    const bool in = own < t1 && j_own < tk;
+    id = in ? ids[own * tk + j_own] : -1;
+    wj = in ? w[own * tk + j_own] : 0.0f;
+    dj = in ? dw[own * tk + j_own] : 0.0f;
+  };
+  fetch(t0);
+  for (int64_t t = t0; t < t1; t += at_once) {
     float s = wj * dj;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    for (int o = 1 << sh >> 1; o > 0; o >>= 1) s += __shfl_xor(s, o);
     const float g = wj * (dj - s);
-    float v[KPER];
+    const int now = id;
+    fetch(t + at_once);
+    const int n = t1 - t < at_once ? (int)(t1 - t) : at_once;
+    float sum[KPER];
 #pragma unroll
-    for (int i = 0; i < KPER; ++i) v[i] = 0.0f;
-    for (int j = 0; j < tk; ++j) {
-      const int ej = __builtin_amdgcn_readlane(id, j);
-      const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), j));
+    for (int i = 0; i < KPER; ++i) sum[i] = 0.0f;
+    for (int r = 0; r < n; ++r) {
+      float v[KPER];
 #pragma unroll
-      for (int i = 0; i < KPER; ++i) v[i] += ej == lane + 64 * i ? gj : 0.0f;
+      for (int i = 0; i < KPER; ++i) v[i] = 0.0f;
+      for (int j = 0; j < tk; ++j) {
+        const int ej = __builtin_amdgcn_readlane(now, (r << sh) + j);
+        const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), (r << sh) + j));
+#pragma unroll
+        for (int i = 0; i < KPER; ++i) v[i] += ej == lane + 64 * i ? gj : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < KPER; ++i) {
+        const int e = lane + 64 * i;
+        if (e < E) d_logits[(t + r) * E + e] = v[i];
+        sum[i] += v[i];
+      }
     }
+    if constexpr (BIAS) {
 #pragma unroll
-    for (int i = 0; i < KPER; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E) d_logits[t * E + e] = v[i];
-      sum[i] += v[i];
+      for (int i = 0; i < KPER; ++i) total[i] += (double)sum[i];
     }
   }
   if constexpr (BIAS) {
-    __shared__ float acc[4][KPER * 64];
+    __shared__ float acc[8][KPER * 64];
 #pragma unroll
-    for (int i = 0; i < KPER; ++i) acc[wave][lane + 64 * i] = sum[i];
+    for (int i = 0; i < KPER; ++i) acc[wave][lane + 64 * i] = (float)total[i];
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 256)
-      part[(int64_t)blockIdx.x * E + e] = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
+    for (int e = threadIdx.x; e < E; e += 512) {
+      double s = 0.0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += (double)acc[q][e];
+      part[(int64_t)blockIdx.x * E + e] = (float)s;
+    }
   }
 }
 
-// d_bias[e] = sum over the workgroups' parts, in a fixed order: wave q of 16
-// takes every 16th, then the sixteen are added.  float64, as the terms of
-// either sign cancel.
+// d_bias[e] = sum over the workgroups' at most 256 parts, in a fixed order: wave
+// q of 16 takes every 16th, all loads at once, then the sixteen are added.
 __global__ void __launch_bounds__(1024)
-k_route_bias(const float* __restrict__ part, int64_t n, int E, float* __restrict__ d_bias) {
+k_route_bias(const float* __restrict__ part, int n, int E, float* __restrict__ d_bias) {
   __shared__ double acc[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = blockIdx.x * 64 + lane;
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int b = wave + 16 * i;
+    v[i] = e < E && b < n ? part[(int64_t)b * E + e] : 0.0f;
+  }
   double s = 0.0;
-  if (e < E)
-    for (int64_t b = wave; b < n; b += 16) s += (double)part[b * E + e];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += (double)v[i];
   acc[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && e < E) {
@@ -122,10 +157,10 @@ k_route_bias(const float* __restrict__ part, int64_t n, int E, float* __restrict
   }
 }
 
-// tokens of a wave: at most 1024 workgroups of four waves, so that the sum of
-// their parts stays short
-static int64_t route_per(int64_t T) { return (T + 4095) / 4096; }
-static int64_t route_blocks(int64_t T) { return (T + 4 * route_per(T) - 1) / (4 * route_per(T)); }
+// tokens of a wave: at most 256 workgroups of eight waves, so that the sum of
+// their parts is one round trip
+static int64_t route_per(int64_t T) { return (T + 2047) / 2048; }
+static int64_t route_blocks(int64_t T) { return (T + 8 * route_per(T) - 1) / (8 * route_per(T)); }
 
 }  // namespace nvfp4
 
@@ -193,16 +228,18 @@ int moe_permute_backward(const int32_t* topk_ids, const float* topk_w, const flo
   NV_REQUIRE(!d_bias || ws_bytes >= moe_permute_backward_workspace_size(T, E), NVFP4_ERR_WORKSPACE,
              "moe_permute_backward: workspace too small");
   const int per = (int)route_per(T);
+  int sh = 0;
+  while (1 << sh < tk) ++sh;
   const int64_t nb = route_blocks(T);
   float* part = static_cast<float*>(ws);
   auto launch = [&](auto kper) {
     constexpr int KP = decltype(kper)::value;
     if (d_bias)
-      k_route_backward<KP, true><<<(unsigned)nb, 256, 0, s>>>(topk_ids, topk_w, d_topk_w, T, (int)E,
-                                                              (int)tk, per, d_logits, part);
+      k_route_backward<KP, true><<<(unsigned)nb, 512, 0, s>>>(topk_ids, topk_w, d_topk_w, T, (int)E,
+                                                              (int)tk, sh, per, d_logits, part);
     else
-      k_route_backward<KP, false><<<(unsigned)nb, 256, 0, s>>>(topk_ids, topk_w, d_topk_w, T, (int)E,
-                                                               (int)tk, per, d_logits, nullptr);
+      k_route_backward<KP, false><<<(unsigned)nb, 512, 0, s>>>(topk_ids, topk_w, d_topk_w, T, (int)E,
+                                                               (int)tk, sh, per, d_logits, nullptr);
   };
   if (E <= 64)
     launch(std::integral_constant<int, 1>{});
@@ -211,7 +248,7 @@ int moe_permute_backward(const int32_t* topk_ids, const float* topk_w, const flo
   else
     launch(std::integral_constant<int, 16>{});
   if (d_bias)
-    k_route_bias<<<(unsigned)((E + 63) / 64), 1024, 0, s>>>(part, nb, (int)E, d_bias);
+    k_route_bias<<<(unsigned)((E + 63) / 64), 1024, 0, s>>>(part, (int)nb, (int)E, d_bias);
   return check_launch("moe_permute_backward");
 }
 
