@@ -210,12 +210,14 @@ constexpr int A_BYTES = BM * 128, W_BYTES = BN * 128, SCALES = (BM + BN) * 16;
 }  // namespace mxb
 
 // The row tiles of all experts, in order: tiles[t] = {expert, first row, rows,
-// 0}, their number in n_tiles[0], and 0 in the eight behind it.  Every workgroup sums the experts' tiles for itself and
-// writes a part of the list.
+// 0}, their number in n_tiles[0], and 0 in the eight behind it.  Every
+// workgroup sums the experts' tiles for itself and writes a part of the list.
+// cap: the list's length, as many as offsets that never decrease can make; of
+// others what goes beyond it is left out.
 __global__ void __launch_bounds__(1024)
-k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles) {
+k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles, int cap) {
   __shared__ int wsum[16];
-  __shared__ int prefix[1025];
+  __shared__ int64_t prefix[1025];
   const int tid = threadIdx.x;
   int v = 0;
   if (tid < p.E) {
@@ -230,12 +232,12 @@ k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles
   }
   if ((tid & 63) == 63) wsum[tid >> 6] = incl;
   __syncthreads();
-  int base = 0;
+  int64_t base = 0;
   for (int w = 0; w < (tid >> 6); ++w) base += wsum[w];
   prefix[tid] = base + incl - v;
   if (tid == 1023) prefix[1024] = base + incl;
   __syncthreads();
-  const int total = prefix[1024];
+  const int total = prefix[1024] < cap ? (int)prefix[1024] : cap;
   for (int t = blockIdx.x * 1024 + tid; t < total; t += gridDim.x * 1024) {
     int lo_e = 0, hi_e = p.E;                            // largest e with prefix[e] <= t
     while (hi_e - lo_e > 1) {
@@ -244,7 +246,7 @@ k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles
     }
     int64_t lo, hi;
     expert_rows(p, lo_e, lo, hi);
-    const int64_t p0 = lo + (int64_t)(t - prefix[lo_e]) * mxb::BM;
+    const int64_t p0 = lo + (t - prefix[lo_e]) * mxb::BM;
     tiles[t] = make_int4(lo_e, (int)p0, (int)(hi - p0 < mxb::BM ? hi - p0 : mxb::BM), 0);
   }
   if (blockIdx.x == 0 && tid < 9) n_tiles[tid] = tid == 0 ? total : 0;
@@ -467,7 +469,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
     }
 
     // NV: blocks of 32 activation rows; x: the stage of the even steps
-    auto run = [&](auto nv_c, uint8_t* const x, uint8_t* const y) {
+    auto run = [&](auto nv_c, uint8_t* const x, uint8_t* const y) __attribute__((always_inline)) {
       constexpr int NV = decltype(nv_c)::value;
       f32x16_t acc[2][NV];
 #pragma unroll
@@ -480,7 +482,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
       // One step, from stage st; the next one's activation rows go to `other`.
       // U: the first or the second of a pair.  LAST: the tile's last, after
       // which comes the next tile's first; HALF: of 128 columns.
-      auto step = [&](int kt, uint8_t* st, uint8_t* other, auto u_c, auto last_c, auto half_c) {
+      auto step = [&](int kt, uint8_t* st, uint8_t* other, auto u_c, auto last_c, auto half_c) __attribute__((always_inline)) {
         constexpr int U = decltype(u_c)::value;
         constexpr bool LAST = decltype(last_c)::value, HALF = decltype(half_c)::value;
         constexpr int S = HALF ? 2 : 4;
@@ -626,13 +628,16 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
     };
     using n4 = std::integral_constant<int, 4>;
     using n2 = std::integral_constant<int, 2>;
-    auto tile = [&](uint8_t* const x, uint8_t* const y) {
+    // (as functions of their own these would have their captures in memory, and
+    // next_v's read was then taken out of the loop that it ends)
+    auto tile = [&](uint8_t* const x, uint8_t* const y) __attribute__((always_inline)) {
       if (cur.valid > 64) run(n4{}, x, y);
       else run(n2{}, x, y);
     };
     if (kOdd && odd) tile(sa1, sa0);
     else tile(sa0, sa1);
     if (!more) return;
+    asm volatile("" ::: "memory");                     // (read here, once per tile)
     v = __builtin_amdgcn_readfirstlane(next_v);
     cur = nxt;
     buf ^= 1;
@@ -703,7 +708,7 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
     int64_t nb = (m_tiles * n_tiles + 7) / 8 * 8;
     if (nb > 2 * num_cus()) nb = (2 * num_cus() + 7) / 8 * 8;
     const int64_t tb = (m_tiles + 1023) / 1024;
-    k_mx_tiles<<<(unsigned)(tb < 256 ? tb : 256), 1024, 0, s>>>(p, tiles, count);
+    k_mx_tiles<<<(unsigned)(tb < 256 ? tb : 256), 1024, 0, s>>>(p, tiles, count, (int)m_tiles);
     if (glu)
       mx_launch_big<true>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
     else

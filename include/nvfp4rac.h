@@ -528,8 +528,12 @@ int mxfp4_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * Requires 1 <= E <= 1024, 0 <= M_total < 2^31, N % 16 == 0 (_swiglu:
  * N % 32 == 0), K % 128 == 0, N and K <= 2^20, the activation's codes and one
  * expert's below 4 GiB; codes, y and ws 16-byte, scales 4-byte aligned; a_rows
- * NULL needs M_src >= M_total.  a_rows entries outside [0, M_src) read its
- * first or last row. */
+ * NULL needs M_src >= M_total; (ceil(M_total/128) + E) * ceil(N/256) < 2^28.
+ * a_rows entries outside [0, M_src) read its first or last row; offsets outside
+ * [0, M_total] count as the nearer end, and where they decrease the rows
+ * concerned are not all written.  ws holds the list of row tiles and the
+ * counters that tiles are taken with: for one call at a time, and nothing of it
+ * is read by the next. */
 size_t grouped_mxfp4_gemm_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* a_rows,
                        int64_t M_src, const uint8_t* w_codes, const uint8_t* w_scales,
@@ -559,8 +563,8 @@ int moe_unpermute_combine_backward(const void* d_out, const void* y, const int32
  *   d_logits[t][topk_ids[t][j]] = w_j (dw_j - sum_i w_i dw_i),  w = topk_w[t],
  *   dw = d_topk_w[t]; 0 for the experts not chosen           [T][E] float32
  *   d_bias[e] = sum_t d_logits[t][e]                [E] float32, or NULL
- * in float32 (d_bias: parts of up to 4 ceil(T/4096) tokens in float32, then
- * float64), in an order that does not depend on timing.  An expert that a token
+ * in float32 (d_bias: sums of up to 64 tokens in float32, these in float64,
+ * at most 2048 and then 256 of them rounded to float32 on the way), in an order that does not depend on timing.  An expert that a token
  * names twice gets the sum of both; ids outside [0, E) write nothing.
  * Requires T >= 0, 1 <= tk <= min(E, 32), E <= 1024, T*tk < 2^31.  T == 0
  * writes d_bias = 0 only.  ws is needed with d_bias alone. */

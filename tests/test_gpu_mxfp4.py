@@ -281,3 +281,39 @@ def test_gemm_of_quantized_tensors_and_input_gradient(dev):
     check(host_vals(y), ref, limits(ref, mag, K), "y")
     ref, mag = OX.grouped_gemm(q(dy), None, np.stack([q(m.T) for m in w]), offs)
     check(host_vals(dx), ref, limits(ref, mag, N), "dx")
+
+
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 768, 896, 1024, 1664])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("glu", [False, True])
+def test_many_tiles_per_workgroup(dev, K, gather, glu):
+    """More tiles than four rounds of the device's workgroups take, for every
+    number of steps at a row's end, against the float64 product."""
+    say(f"mxfp4 many tiles K={K} gather={gather} glu={glu}")
+    g = torch.Generator("cuda").manual_seed(K)
+    counts = [3000, 1, 70, 2500, 0, 130]
+    N, E, P = 12288, len(counts), sum(counts)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)     # noqa: E731
+    M_src = 4000 if gather else P
+    a, w = F.mxfp4_quantize(rand(M_src, K)), F.mxfp4_quantize(rand(E, N, K))
+    rows = torch.randint(0, M_src, (P,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    call = F.grouped_mxfp4_gemm_swiglu if glu else F.grouped_mxfp4_gemm
+    got = call(*a, rows, *w, cu(offsets_of(counts)))
+    av, wv = F.mxfp4_restore(*a).double(), F.mxfp4_restore(*w).double()
+    offs = offsets_of(counts)
+    for e in range(E):
+        lo, hi = int(offs[e]), int(offs[e + 1])
+        if lo == hi:
+            continue
+        ae = av[rows[lo:hi].long()] if gather else av[lo:hi]
+        we = wv[e].t().contiguous()
+        y, mag = ae @ we, ae.abs() @ we.abs()
+        d = K * 2.0 ** -23 * mag
+        if glu:                                          # (swiglu_limits)
+            (gt, u), (dg, du) = y.chunk(2, 1), d.chunk(2, 1)
+            y = gt * torch.sigmoid(gt) * u
+            rel = 2.0 ** -21 + 1.45 * gt.abs() * 2.0 ** -24
+            d = 1.1 * u.abs() * dg + (gt.abs() + 1.1 * dg) * du + rel * y.abs()
+        lim = d + 2.0 ** -8 * (y.abs() + d) + 2.0 ** -120
+        off = (got[lo:hi].double() - y).abs()
+        assert bool((off <= lim).all()), (e, int((off > lim).sum()))

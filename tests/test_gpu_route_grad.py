@@ -4,8 +4,9 @@ moe_permute_backward) against the float64 oracle.
 Tolerances, from the arithmetic.  dy is one float32 product (2^-24) rounded to
 bf16 (2^-8).  d_topk_w is a float32 sum of N exact products: N * 2^-24 of the
 sum of magnitudes.  A logit's gradient w (dw - sum w dw) has tk + 1 terms, each
-a product: (tk + 3) * 2^-24 of w (|dw| + sum |w dw|).  d_bias adds up to 4
-ceil(T / 4096) of them in float32 and rounds the float64 sum of those once."""
+a product: (tk + 3) * 2^-24 of w (|dw| + sum |w dw|).  d_bias adds
+ceil(T / 2048) of them in float32 and rounds the float64 sums of those three
+times (a wave's, a workgroup's, the whole): 4 ceil(T / 4096) roundings or fewer."""
 import sys
 
 import numpy as np
