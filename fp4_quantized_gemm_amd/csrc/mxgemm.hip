@@ -266,7 +266,10 @@ __device__ __forceinline__ f32x16_t mfma32_mx4(const u32x4& a, uint32_t sa, cons
 // of LDS; then every wave's
 template <int N>
 __device__ __forceinline__ void mx_wait() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  // vmcnt(N) lgkmcnt(0), in a form that the compiler counts with
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | (7 << 4));
+  asm volatile("" ::: "memory");
 }
 __device__ __forceinline__ void mx_barrier() {
   __builtin_amdgcn_s_barrier();
@@ -276,6 +279,16 @@ __device__ __forceinline__ void mx_barrier() {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_buffer(const void* p, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)(uint32_t)bytes,
                                            kBufferRsrcWord3);
+}
+
+// N stores that go nowhere, behind what was issued before
+template <int N>
+__device__ __forceinline__ void mx_no_stores(uint16_t* y) {
+  const __amdgpu_buffer_rsrc_t none = mx_buffer(y, 0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, none, 16u * i, 0, 2);
 }
 
 struct MxTile {
@@ -323,7 +336,10 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
   if (v >= end) return;
   MxTile cur = mx_tile(tiles, real_m, n_tiles, v);
   v += stride;                                          // the next one
-  int32_t* const tickets = n_row_tiles + 1 + (blockIdx.x & 7);
+  // (an index that looks different per lane: of a common address the compiler
+  // makes one atomic for the wave, and waits for it at once)
+  uint32_t ticket_at = 1 + (blockIdx.x & 7);
+  asm volatile("" : "+v"(ticket_at));
 
   const uint32_t KC = (uint32_t)(p.K / 2), KS = (uint32_t)(p.K / 32);
   const int nd = (int)(p.K / 128);                      // dwords of a row's scales
@@ -455,17 +471,20 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
   issue_a(sa0, 0);
   issue_w(0);
 
-  constexpr int kStores = GLU ? 8 : 16;                 // of a whole tile, per wave
-  int stores = 0;                                       // the last tile's
+  // Every tile ends with as many stores, and one comes before the first tile
+  // (those of rows that are not there go nowhere), so that a tile's first step
+  // waits for what was loaded before them and not for them.
+  constexpr int kStores = GLU ? 8 : 16;
+  mx_no_stores<kStores>(p.y);
   bool odd = false;                                     // the tile's first step is in sa1
   for (;;) {
     const bool more = v < end;
     MxTile nxt = cur;
-    int ticket = 0;
+    int ticket;
     if (more) {
       nxt = mx_tile(tiles, real_m, n_tiles, v);
       if (p.a_rows) issue_rows(nxt, rows[buf ^ 1]);
-      if (tid == 0) ticket = atomicAdd(tickets, 1);
+      if (tid == 0) ticket = atomicAdd(n_row_tiles + ticket_at, 1);
     }
 
     // NV: blocks of 32 activation rows; x: the stage of the even steps
@@ -487,9 +506,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
         constexpr bool LAST = decltype(last_c)::value, HALF = decltype(half_c)::value;
         constexpr int S = HALF ? 2 : 4;
         if (kt > 0 || ns == 1) mx_wait<0>();
-        else if (stores == kStores) mx_wait<kStores>();
-        else if (stores) mx_wait<kStores / 2>();
-        else mx_wait<0>();
+        else mx_wait<kStores>();
         mx_barrier();
         if constexpr (U == 0) {
           // dword 2 u + q of the step u of the pair (HALF: 2 u, and two of its
@@ -610,6 +627,8 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
               *reinterpret_cast<uint2*>(own + (r * (16 * LR) + (piece << 4) + half * 8)) =
                   make_uint2(u[0], u[1]);
             }
+          // (other lanes have written what is read next)
+          asm volatile("" ::: "memory");
 #pragma unroll
           for (int t = 0; t < LR / 2; ++t) {
             const int row = (64 / LR) * t + l / LR, c = l % LR;
@@ -624,7 +643,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
         }
       };
       put((kOdd ? x : y) + 4096 * wave);
-      stores = NV * (kStores / 4);
+      mx_no_stores<(4 - NV) * (kStores / 4)>(p.y);
     };
     using n4 = std::integral_constant<int, 4>;
     using n2 = std::integral_constant<int, 2>;
