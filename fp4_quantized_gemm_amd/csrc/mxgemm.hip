@@ -41,11 +41,17 @@ __device__ __forceinline__ f32x4_t mfma16_mx4(const u32x4& a, uint32_t sa, const
 }
 
 // The rows of expert e, within the output.
-__device__ __forceinline__ void expert_rows(const MxGemmArgs& p, int e, int64_t& lo, int64_t& hi) {
-  lo = p.offsets[e];
-  hi = p.offsets[e + 1];
-  lo = lo < 0 ? 0 : (lo > p.M_total ? p.M_total : lo);
-  hi = hi < lo ? lo : (hi > p.M_total ? p.M_total : hi);
+__device__ __forceinline__ void clamp_rows(int M_total, int& lo, int& hi) {
+  lo = max(0, min(lo, M_total));
+  hi = max(lo, min(hi, M_total));
+}
+__device__ __forceinline__ void expert_rows(const MxGemmArgs& p, int e, int& lo, int& hi) {
+  // (of the wave's one expert: scalar loads, that wait for no vector load or store)
+  typedef const int32_t __attribute__((address_space(4))) * scalar_ptr;
+  const scalar_ptr offsets = (scalar_ptr)p.offsets;
+  lo = offsets[e];
+  hi = offsets[e + 1];
+  clamp_rows((int)p.M_total, lo, hi);
 }
 
 __device__ __forceinline__ int64_t source_row(const MxGemmArgs& p, int64_t row) {
@@ -55,27 +61,28 @@ __device__ __forceinline__ int64_t source_row(const MxGemmArgs& p, int64_t row) 
 
 // ------------------------------------------------------------------------
 // Small products, without LDS: a wave owns 16 weight rows (GLU: 16 gate rows and
-// the same 16 up rows) and multiplies all of K with one or two tiles of 16
-// activation rows, operands straight from memory to registers.  K advances in
-// chunks of 512, the next one under way while one is multiplied.  Lane (r, q)
-// takes the 16-byte pieces 4 s + q, s = 0 .. 3, of its row's 256 bytes, and the
-// chunk's 16 scale bytes, of which byte q of dword s belongs to piece s.
+// the same 16 up rows) and multiplies all of K with a tile of 16 activation
+// rows, operands straight from memory to registers.  K advances in chunks of
+// 512, the next one under way while one is multiplied.  Lane (r, q) takes the
+// 16-byte pieces 4 s + q, s = 0 .. 3, of its row's 256 bytes, and the chunk's 16
+// scale bytes, of which byte q of dword s belongs to piece s.
 //
-// Bound by latency: one launch and a few round trips.  It is taken where all
-// experts' tiles of 16 rows times 64 columns are at most 512: one token's 8
-// experts of 4096x1536 (512 tiles) 11.4 us, 16 rows for each of 8 of them 12.8
-// against 15.5 with the large tiles (two launches), 64 rows for each of 4 of
-// 1536x2048 (384) 13.5 against 15.8; beyond, 48 rows for each of 8 of 1536x2048
-// (576) 15.7 against 15.7, 128 rows for each of 4 (768) 19.9 against 16.2, 16
-// rows for each of 128 58 against 49.
+// Bound by latency: a round trip per chunk, in as many workgroups as there are
+// tiles (two tiles of rows per wave, weights read once: 128 rows of one
+// 4096x1536 7.0 us against 8.2, but 32 rows for each of 4 of 1536x8192 43
+// against 32, 64 rows of one of it 28.5 against 19.6).  Taken for at most 512
+// tiles of 16 rows x 64 columns.  Times in a graph, against the large tiles: 64
+// rows of one 512x512 3.2 us, 6.0; 4 rows for each of 8 of 4096x1536 (512 tiles)
+// 8.1, 10.8, one row of it 11.1, 11.2; 64 for each of 4 of 1536x2048 (432) 10.3,
+// 11.5; beyond, 32 rows for each of 4 of 4096x1536 (640) 10.3, 9.7; 16 for each
+// of 8 of it (768) 12.5, 11.0; 16 for each of 128 of it 137, 87.
 // ------------------------------------------------------------------------
-// R: groups of 16 weight rows, TT: tiles of activation rows
-template <int R, int TT>
-struct MxChunk {
-  u32x4 w[R][4], sw[R], a[TT][4], sa[TT];
+template <int R>
+struct MxChunk {                                        // R: groups of 16 weight rows
+  u32x4 w[R][4], sw[R], a[4], sa;
 };
 
-template <int TT, bool GLU>
+template <bool GLU>
 __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t p0, int64_t hi) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -85,15 +92,10 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
   const int64_t KC = p.K / 2, KS = p.K / 32;
   const int nd = (int)(p.K / 128), nch = (nd + 3) / 4;
   const int64_t n0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
-  const uint8_t* ac[TT];
-  const uint8_t* asc[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t row = p0 + 16 * t + r16;
-    const int64_t src = source_row(p, row < hi ? row : hi - 1);
-    ac[t] = p.a_codes + src * KC + 16 * q;
-    asc[t] = p.a_scales + src * KS;
-  }
+  const int64_t row = p0 + r16;
+  const int64_t src = source_row(p, row < hi ? row : hi - 1);
+  const uint8_t* const ac = p.a_codes + src * KC + 16 * q;
+  const uint8_t* const asc = p.a_scales + src * KS;
   const uint8_t* wc[R];
   const uint8_t* wsc[R];
 #pragma unroll
@@ -105,7 +107,7 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
     wsc[g] = p.w_scales + ((int64_t)e * p.N + n) * KS;
   }
   typedef u32x4 u32x4a __attribute__((aligned(4)));     // (rows of scales are whole dwords)
-  using Chunk = MxChunk<R, TT>;
+  using Chunk = MxChunk<R>;
   auto load = [&](Chunk& k, int c) {
     const int m = nd - 4 * c;                           // pieces that are there, if fewer than 4
     const int64_t kc = 256 * c, ks = 16 * c;
@@ -123,14 +125,11 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
     };
 #pragma unroll
     for (int g = 0; g < R; ++g) row(k.w[g], k.sw[g], wc[g], wsc[g]);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) row(k.a[t], k.sa[t], ac[t], asc[t]);
+    row(k.a, k.sa, ac, asc);
   };
-  f32x4_t acc[R][TT];
+  f32x4_t acc[R];
 #pragma unroll
-  for (int g = 0; g < R; ++g)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[g][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int g = 0; g < R; ++g) acc[g] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const Chunk& k, int c) {
     const int m = nd - 4 * c;
 #pragma unroll
@@ -138,10 +137,7 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
       if (s < m) {
 #pragma unroll
         for (int g = 0; g < R; ++g)
-#pragma unroll
-          for (int t = 0; t < TT; ++t)
-            acc[g][t] = mfma16_mx4(k.w[g][s], k.sw[g][s] >> (8 * q), k.a[t][s], k.sa[t][s] >> (8 * q),
-                                   acc[g][t]);
+          acc[g] = mfma16_mx4(k.w[g][s], k.sw[g][s] >> (8 * q), k.a[s], k.sa[s] >> (8 * q), acc[g]);
       }
   };
   Chunk k0, k1;
@@ -154,30 +150,25 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
       multiply(k1, c + 1);
     }
   }
-  // lane (r, q): columns n0 + 4 q .. + 3 of row p0 + 16 t + r
+  // lane (r, q): columns n0 + 4 q .. + 3 of row p0 + r
   const int64_t n = n0 + 4 * q;
+  if (row >= hi || n >= NO) return;
+  f32x4_t v = acc[0];
+  if constexpr (GLU) {
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    const int64_t row = p0 + 16 * t + r16;
-    if (row >= hi || n >= NO) continue;
-    f32x4_t v = acc[0][t];
-    if constexpr (GLU) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[1][t][i]);
-    }
-    *reinterpret_cast<uint2*>(p.y + row * NO + n) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+    for (int i = 0; i < 4; ++i) v[i] = silu_mul(v[i], acc[1][i]);
   }
+  *reinterpret_cast<uint2*>(p.y + row * NO + n) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
 }
 
 template <bool GLU>
 __global__ void __launch_bounds__(256, 2)
 k_mx_few(MxGemmArgs p) {
   const int e = blockIdx.y;
-  int64_t lo, hi;
+  int lo, hi;
   expert_rows(p, e, lo, hi);
-  int64_t p0 = lo + (int64_t)blockIdx.z * 32;
-  for (; p0 + 16 < hi; p0 += (int64_t)gridDim.z * 32) mx_few_tile<2, GLU>(p, e, p0, hi);
-  if (p0 < hi) mx_few_tile<1, GLU>(p, e, p0, hi);
+  for (int64_t p0 = lo + (int64_t)blockIdx.z * 16; p0 < hi; p0 += (int64_t)gridDim.z * 16)
+    mx_few_tile<GLU>(p, e, p0, hi);
 }
 
 // ------------------------------------------------------------------------
@@ -208,49 +199,6 @@ namespace mxb {
 constexpr int BM = 128, BN = 256;
 constexpr int A_BYTES = BM * 128, W_BYTES = BN * 128, SCALES = (BM + BN) * 16;
 }  // namespace mxb
-
-// The row tiles of all experts, in order: tiles[t] = {expert, first row, rows,
-// 0}, their number in n_tiles[0], and 0 in the eight behind it.  Every
-// workgroup sums the experts' tiles for itself and writes a part of the list.
-// cap: the list's length, as many as offsets that never decrease can make; of
-// others what goes beyond it is left out.
-__global__ void __launch_bounds__(1024)
-k_mx_tiles(MxGemmArgs p, int4* __restrict__ tiles, int32_t* __restrict__ n_tiles, int cap) {
-  __shared__ int wsum[16];
-  __shared__ int64_t prefix[1025];
-  const int tid = threadIdx.x;
-  int v = 0;
-  if (tid < p.E) {
-    int64_t lo, hi;
-    expert_rows(p, tid, lo, hi);
-    v = (int)((hi - lo + mxb::BM - 1) / mxb::BM);
-  }
-  int incl = v;
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(incl, o);
-    if ((tid & 63) >= o) incl += u;
-  }
-  if ((tid & 63) == 63) wsum[tid >> 6] = incl;
-  __syncthreads();
-  int64_t base = 0;
-  for (int w = 0; w < (tid >> 6); ++w) base += wsum[w];
-  prefix[tid] = base + incl - v;
-  if (tid == 1023) prefix[1024] = base + incl;
-  __syncthreads();
-  const int total = prefix[1024] < cap ? (int)prefix[1024] : cap;
-  for (int t = blockIdx.x * 1024 + tid; t < total; t += gridDim.x * 1024) {
-    int lo_e = 0, hi_e = p.E;                            // largest e with prefix[e] <= t
-    while (hi_e - lo_e > 1) {
-      const int mid = (lo_e + hi_e) >> 1;
-      if (prefix[mid] <= t) lo_e = mid; else hi_e = mid;
-    }
-    int64_t lo, hi;
-    expert_rows(p, lo_e, lo, hi);
-    const int64_t p0 = lo + (t - prefix[lo_e]) * mxb::BM;
-    tiles[t] = make_int4(lo_e, (int)p0, (int)(hi - p0 < mxb::BM ? hi - p0 : mxb::BM), 0);
-  }
-  if (blockIdx.x == 0 && tid < 9) n_tiles[tid] = tid == 0 ? total : 0;
-}
 
 // D += 2^(sa - 127 + sb - 127) A B over 64 k: lane (r = l % 32, q = l / 32)
 // has 32 codes of row r in 16 bytes, byte SEL of sa / sb their scale
@@ -295,38 +243,84 @@ struct MxTile {
   int e, p0, valid, nt;
 };
 
+// prefix[e] = row tiles of the experts before e, for e = 0 .. 1024, at most cap:
+// as many as offsets that never decrease can make; of others what goes beyond is
+// left out.  scratch: 4 words.
+__device__ __forceinline__ void mx_count_tiles(const MxGemmArgs& p, int cap, int32_t* prefix,
+                                               int32_t* scratch) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int off[5], n[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) off[i] = p.offsets[min(4 * tid + i, p.E)];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int lo = off[i], hi = off[i + 1];
+    clamp_rows((int)p.M_total, lo, hi);
+    n[i] = 4 * tid + i < p.E ? (int)((uint32_t)(hi - lo + mxb::BM - 1) / mxb::BM) : 0;
+    sum = min(sum + n[i], cap);
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(incl, o);
+    if (lane >= o) incl = min(incl + u, cap);
+  }
+  int before = __shfl_up(incl, 1);
+  if (lane == 0) before = 0;
+  if (lane == 63) scratch[wave] = incl;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) before = min(before + scratch[w], cap);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    prefix[4 * tid + i] = before;
+    before = min(before + n[i], cap);
+  }
+  if (tid == 255) prefix[1024] = before;
+  __syncthreads();
+}
+
 // Tile v in the order: groups of 8 row tiles x all column tiles, row tiles
-// fastest.
-__device__ __forceinline__ MxTile mx_tile(const int4* __restrict__ tiles, int real_m, int n_tiles,
-                                          int v) {
+// fastest.  The row tile's expert, the last whose prefix is not beyond it, is
+// found in two steps of 64 and 16 lanes.
+__device__ __forceinline__ MxTile mx_tile(const MxGemmArgs& p, const int32_t* prefix, int real_m,
+                                          int n_tiles, int v) {
   constexpr int G = 8;
   const int gi = v / (G * n_tiles), gr = v - gi * G * n_tiles;
   const int gm = real_m - G * gi < G ? real_m - G * gi : G;
-  const int nt = gr / gm;
-  const int4 t = tiles[G * gi + gr - nt * gm];
-  return {t.x, t.y, t.z, nt};
+  const int nt = gr / gm, t = G * gi + gr - nt * gm;
+  const int lane = threadIdx.x & 63;
+  const uint64_t m1 = __ballot(16 * lane < p.E && prefix[16 * lane] <= t);
+  const int e1 = 16 * (__builtin_popcountll(m1) - 1) + (lane & 15);
+  const int at = prefix[e1];
+  const uint64_t m2 = __ballot(lane < 16 && e1 < p.E && at <= t);
+  const int l2 = __builtin_popcountll(m2) - 1;
+  const int e = __builtin_amdgcn_readlane(e1, l2);
+  int lo, hi;
+  expert_rows(p, e, lo, hi);
+  const int p0 = lo + (t - __builtin_amdgcn_readlane(at, l2)) * mxb::BM;
+  return {e, p0, min(hi - p0, mxb::BM), nt};
 }
 
 // ND: K / 128 modulo 4, so what the last steps are
 template <bool GLU, int ND>
 __global__ void __launch_bounds__(256, 2)
-k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_row_tiles,
-         int n_tiles) {
+k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
   using namespace mxb;
   // separate objects, each access naming its own: the compiler then does not
   // wait for loads into the others
   __shared__ __attribute__((aligned(16))) uint8_t sa0[A_BYTES], sa1[A_BYTES], sw[W_BYTES], ssc[SCALES];
-  __shared__ int32_t rows[2][BM], next_v;
+  __shared__ int32_t rows[2][BM], prefix[1025], next_v;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 5, r32 = lane & 31;
 
   // each XCD (workgroup b runs on XCD b % 8) takes a contiguous range of the
-  // tiles, so its L2 holds an expert's weights; its workgroups start with one
-  // each and a second, then take the next that nobody has (which workgroup
-  // computes a tile does not show in it)
-  const int real_m = *n_row_tiles;
+  // tiles, so its L2 holds an expert's weights; its workgroups take every
+  // stride-th, or (taken: eight counters, 0 at first) after two each the next
+  // that nobody has (which workgroup computes a tile does not show in it)
+  mx_count_tiles(p, max_m, prefix, rows[0]);
+  const int real_m = __builtin_amdgcn_readfirstlane(prefix[1024]);
   const int total = real_m * n_tiles;
   const int per_xcd = (total + 7) / 8;
   const int first = ((int)blockIdx.x & 7) * per_xcd;
@@ -334,11 +328,11 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
   const int stride = (int)gridDim.x >> 3;
   int v = first + ((int)blockIdx.x >> 3);
   if (v >= end) return;
-  MxTile cur = mx_tile(tiles, real_m, n_tiles, v);
+  MxTile cur = mx_tile(p, prefix, real_m, n_tiles, v);
   v += stride;                                          // the next one
   // (an index that looks different per lane: of a common address the compiler
   // makes one atomic for the wave, and waits for it at once)
-  uint32_t ticket_at = 1 + (blockIdx.x & 7);
+  uint32_t ticket_at = blockIdx.x & 7;
   asm volatile("" : "+v"(ticket_at));
 
   const uint32_t KC = (uint32_t)(p.K / 2), KS = (uint32_t)(p.K / 32);
@@ -482,9 +476,9 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
     MxTile nxt = cur;
     int ticket;
     if (more) {
-      nxt = mx_tile(tiles, real_m, n_tiles, v);
+      nxt = mx_tile(p, prefix, real_m, n_tiles, v);
       if (p.a_rows) issue_rows(nxt, rows[buf ^ 1]);
-      if (tid == 0) ticket = atomicAdd(n_row_tiles + ticket_at, 1);
+      if (taken && tid == 0) ticket = atomicAdd(taken + ticket_at, 1);
     }
 
     // NV: blocks of 32 activation rows; x: the stage of the even steps
@@ -542,7 +536,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
         const bool ahead = !LAST || more;
         if (LAST && more) {
           aim(nxt, rows[buf ^ 1]);
-          if (tid == 0) next_v = first + 2 * stride + ticket;
+          if (taken && tid == 0) next_v = first + 2 * stride + ticket;
         }
         if (ahead) issue_a(other, LAST ? 0 : kt + 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -657,7 +651,7 @@ k_mx_big(MxGemmArgs p, const int4* __restrict__ tiles, int32_t* __restrict__ n_r
     else tile(sa0, sa1);
     if (!more) return;
     asm volatile("" ::: "memory");                     // (read here, once per tile)
-    v = __builtin_amdgcn_readfirstlane(next_v);
+    v = taken ? __builtin_amdgcn_readfirstlane(next_v) : v + stride;
     cur = nxt;
     buf ^= 1;
     odd = !odd;
@@ -674,13 +668,13 @@ static int64_t mx_row_tiles(int64_t E, int64_t M_total) {
 }
 
 template <bool GLU>
-static void mx_launch_big(unsigned nb, hipStream_t s, const MxGemmArgs& p, const int4* tiles,
-                          int32_t* count, int n_tiles) {
+static void mx_launch_big(unsigned nb, hipStream_t s, const MxGemmArgs& p, int32_t* taken, int max_m,
+                          int n_tiles) {
   switch ((p.K / 128) % 4) {
-    case 0: k_mx_big<GLU, 0><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
-    case 1: k_mx_big<GLU, 1><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
-    case 2: k_mx_big<GLU, 2><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
-    default: k_mx_big<GLU, 3><<<nb, 256, 0, s>>>(p, tiles, count, n_tiles); break;
+    case 0: k_mx_big<GLU, 0><<<nb, 256, 0, s>>>(p, taken, max_m, n_tiles); break;
+    case 1: k_mx_big<GLU, 1><<<nb, 256, 0, s>>>(p, taken, max_m, n_tiles); break;
+    case 2: k_mx_big<GLU, 2><<<nb, 256, 0, s>>>(p, taken, max_m, n_tiles); break;
+    default: k_mx_big<GLU, 3><<<nb, 256, 0, s>>>(p, taken, max_m, n_tiles); break;
   }
 }
 
@@ -715,26 +709,35 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
                static_cast<uint16_t*>(y), M_src, M_total, N, K, (int)E};
   hipStream_t s = as_stream(stream);
   const int64_t NO = glu ? N / 2 : N;
-  // small: tiles of 16 rows of the experts that can have rows, times 64 columns
+  // small: tiles of 16 rows (and half a one more for each expert that can have
+  // rows) times 64 columns
   const int64_t blocks = (NO + 63) / 64, tiles16 = (M_total + 15) / 16;
   const int64_t active = M_total < E ? M_total : E;
-  if (blocks * (tiles16 > active ? tiles16 : active) > 512) {
+  const int64_t likely = tiles16 + active / 2;
+  if (blocks * (likely > active ? likely : active) > 512) {
     const int64_t n_tiles = (N + mxb::BN - 1) / mxb::BN, m_tiles = mx_row_tiles(E, M_total);
     NV_REQUIRE(m_tiles * n_tiles < (1 << 28), NVFP4_ERR_UNSUPPORTED, "%s: too many tiles", name);
-    int32_t* count = static_cast<int32_t*>(ws);
-    int4* tiles = reinterpret_cast<int4*>(static_cast<char*>(ws) + 256);
     // two workgroups per CU, a multiple of the XCDs
     int64_t nb = (m_tiles * n_tiles + 7) / 8 * 8;
     if (nb > 2 * num_cus()) nb = (2 * num_cus() + 7) / 8 * 8;
-    const int64_t tb = (m_tiles + 1023) / 1024;
-    k_mx_tiles<<<(unsigned)(tb < 256 ? tb : 256), 1024, 0, s>>>(p, tiles, count, (int)m_tiles);
+    // Tiles taken as workgroups get free where one has more than 72 steps: 33
+    // tiles of 6 steps each (128 experts of 4096x1536, 1024 rows each) 565 us
+    // against 616, 5 of 16 (32 of 4096x4096, 512 rows) 198 against 205; 8 of 8
+    // (8 of 4096x2048, 4096 rows, SwiGLU) 157 against 154, 4 of 6 (128 of
+    // 4096x1536, 16 rows) 91 against 87.5, as the counters have to be cleared.
+    int32_t* taken = nullptr;
+    if (m_tiles * n_tiles * ((K + 255) / 256) > 72 * nb) {
+      taken = static_cast<int32_t*>(ws);
+      fill_u32(reinterpret_cast<uint32_t*>(taken), 8, 0u, s);
+    }
     if (glu)
-      mx_launch_big<true>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
+      mx_launch_big<true>((unsigned)nb, s, p, taken, (int)m_tiles, (int)n_tiles);
     else
-      mx_launch_big<false>((unsigned)nb, s, p, tiles, count, (int)n_tiles);
+      mx_launch_big<false>((unsigned)nb, s, p, taken, (int)m_tiles, (int)n_tiles);
     return check_launch(name);
   }
-  const int64_t z = ((M_total + E - 1) / E + 31) / 32;  // (at most 1024: 512 tiles of 16 rows)
+  // (twice the mean: an expert with more rows than others has its tiles side by side too)
+  const int64_t z2 = 2 * (((M_total + E - 1) / E + 15) / 16), z = z2 < tiles16 ? z2 : tiles16;
   const dim3 grid((unsigned)blocks, (unsigned)E, (unsigned)z);
   if (glu)
     k_mx_few<true><<<grid, 256, 0, s>>>(p);
@@ -746,9 +749,8 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
 extern "C" {
 
 size_t grouped_mxfp4_gemm_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K) {
-  (void)N, (void)K;
-  if (E < 1 || E > 1024 || M_total < 0 || M_total >= (1LL << 31)) return 256;
-  return 256 + round_up((size_t)mx_row_tiles(E, M_total) * sizeof(int4), 256);
+  (void)E, (void)M_total, (void)N, (void)K;
+  return 256;                                           // eight counters
 }
 
 int grouped_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* a_rows,

@@ -531,9 +531,9 @@ int mxfp4_restore(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_
  * NULL needs M_src >= M_total; (ceil(M_total/128) + E) * ceil(N/256) < 2^28.
  * a_rows entries outside [0, M_src) read its first or last row; offsets outside
  * [0, M_total] count as the nearer end, and where they decrease the rows
- * concerned are not all written.  ws holds the list of row tiles and the
- * counters that tiles are taken with: for one call at a time, and nothing of it
- * is read by the next. */
+ * concerned are not all written.  ws holds the counters that
+ * tiles are taken with: for one call at a time, and nothing of it is read by the
+ * next. */
 size_t grouped_mxfp4_gemm_workspace_size(int64_t E, int64_t M_total, int64_t N, int64_t K);
 int grouped_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const int32_t* a_rows,
                        int64_t M_src, const uint8_t* w_codes, const uint8_t* w_scales,

@@ -283,11 +283,12 @@ def test_gemm_of_quantized_tensors_and_input_gradient(dev):
     check(host_vals(dx), ref, limits(ref, mag, N), "dx")
 
 
-@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 768, 896, 1024, 1664])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 768, 896, 1024, 1664, 4096, 4224, 4352, 4480])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("glu", [False, True])
 def test_many_tiles_per_workgroup(dev, K, gather, glu):
-    """More tiles than four rounds of the device's workgroups take, for every
+    """More tiles than four rounds of the device's workgroups take (from K = 4096:
+    taken as they get free), for every
     number of steps at a row's end, against the float64 product."""
     say(f"mxfp4 many tiles K={K} gather={gather} glu={glu}")
     g = torch.Generator("cuda").manual_seed(K)
