@@ -70,12 +70,12 @@ __device__ __forceinline__ int64_t source_row(const MxGemmArgs& p, int64_t row) 
 // Bound by latency: a round trip per chunk, in as many workgroups as there are
 // tiles (two tiles of rows per wave, weights read once: 128 rows of one
 // 4096x1536 7.0 us against 8.2, but 32 rows for each of 4 of 1536x8192 43
-// against 32, 64 rows of one of it 28.5 against 19.6).  Taken for at most 512
+// against 21, 64 rows of one of it 28.5 against 19.6).  Taken for at most 512
 // tiles of 16 rows x 64 columns.  Times in a graph, against the large tiles: 64
-// rows of one 512x512 3.2 us, 6.0; 4 rows for each of 8 of 4096x1536 (512 tiles)
-// 8.1, 10.8, one row of it 11.1, 11.2; 64 for each of 4 of 1536x2048 (432) 10.3,
-// 11.5; beyond, 32 rows for each of 4 of 4096x1536 (640) 10.3, 9.7; 16 for each
-// of 8 of it (768) 12.5, 11.0; 16 for each of 128 of it 137, 87.
+// rows of one 512x512 3.2 us, 6.0; one row for each of 8 of 128 experts of
+// 4096x1536 (512 tiles) 8.3, 11.2; 4 rows for each of 8 of it (512) 8.6, 10.8;
+// 64 for each of 4 of 1536x2048 (432) 11.0, 11.5; beyond, 32 rows for each of 4
+// of 4096x1536 (640) 11.7, 9.7; 16 for each of 8 of it (768) 12.3, 11.0.
 // ------------------------------------------------------------------------
 template <int R>
 struct MxChunk {                                        // R: groups of 16 weight rows
@@ -161,14 +161,54 @@ __device__ __forceinline__ void mx_few_tile(const MxGemmArgs& p, int e, int64_t 
   *reinterpret_cast<uint2*>(p.y + row * NO + n) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
 }
 
+// Workgroup (x, y): columns 64 x .. 64 x + 63 of the y-th tile of 16 rows.  Every
+// wave counts the experts' tiles, `per` experts to a lane, and looks its own up:
+// a grid over the experts would have 8192 workgroups for one token's 8 of 128
+// (11.1 us in a graph against 8.3; 0.5 us less for up to 8 experts).
 template <bool GLU>
 __global__ void __launch_bounds__(256, 2)
 k_mx_few(MxGemmArgs p) {
-  const int e = blockIdx.y;
-  int lo, hi;
-  expert_rows(p, e, lo, hi);
-  for (int64_t p0 = lo + (int64_t)blockIdx.z * 16; p0 < hi; p0 += (int64_t)gridDim.z * 16)
-    mx_few_tile<GLU>(p, e, p0, hi);
+  const int lane = threadIdx.x & 63, y = blockIdx.y;
+  if (p.E == 1) {
+    int lo, hi;
+    expert_rows(p, 0, lo, hi);
+    if (16 * y < hi - lo) mx_few_tile<GLU>(p, 0, lo + 16 * y, hi);
+    return;
+  }
+  const int per = (p.E + 63) / 64;
+  int n = 0;
+  for (int i0 = 0; i0 < per; i0 += 4) {
+    int off[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) off[i] = p.offsets[min(lane * per + min(i0 + i, per), p.E)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int lo = off[i], hi = off[i + 1];                 // (past the lane's last: the same)
+      clamp_rows((int)p.M_total, lo, hi);
+      n += (hi - lo + 15) / 16;
+    }
+  }
+  int incl = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(incl, o);
+    if (lane >= o) incl += u;
+  }
+  const uint64_t mine = __ballot(incl > y);
+  if (!mine) return;
+  const int l = __builtin_ctzll(mine);
+  int t = y - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(n, l));
+  const int last = min((l + 1) * per, p.E);
+  for (int e = l * per; e < last; ++e) {
+    int lo, hi;
+    expert_rows(p, e, lo, hi);
+    const int tiles = (hi - lo + 15) / 16;
+    if (t < tiles) {
+      mx_few_tile<GLU>(p, e, lo + 16 * t, hi);
+      return;
+    }
+    t -= tiles;
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -736,9 +776,8 @@ static int mx_gemm(const char* name, bool glu, const uint8_t* a_codes, const uin
       mx_launch_big<false>((unsigned)nb, s, p, taken, (int)m_tiles, (int)n_tiles);
     return check_launch(name);
   }
-  // (twice the mean: an expert with more rows than others has its tiles side by side too)
-  const int64_t z2 = 2 * (((M_total + E - 1) / E + 15) / 16), z = z2 < tiles16 ? z2 : tiles16;
-  const dim3 grid((unsigned)blocks, (unsigned)E, (unsigned)z);
+  // as many tiles of 16 rows as there can be
+  const dim3 grid((unsigned)blocks, (unsigned)(M_total / 16 + active));
   if (glu)
     k_mx_few<true><<<grid, 256, 0, s>>>(p);
   else
