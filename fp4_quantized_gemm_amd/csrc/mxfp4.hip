@@ -59,9 +59,9 @@ k_mx4_quantize(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t ldx
 
 // Codes of the transpose: blocks of 32 rows of x, one column each.  A
 // workgroup takes 256 rows x 64 columns through LDS; then each lane has two
-// columns of one block of 32 rows (the dwords of a row's 64 columns are
-// read by consecutive lanes: no bank conflicts), so a column's 8 blocks are
-// 128 contiguous bytes of codes.
+// columns of one block of 32 rows, and the 8 lanes of a column's 8 blocks write
+// 128 contiguous bytes of codes.  (A block's rows are rotated by 8 dwords more
+// than those of the block before: the lanes of a read take every bank alike.)
 constexpr int kTM = 256, kTK = 64;
 __global__ void __launch_bounds__(256)
 k_mx4_quantize_t(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
@@ -77,12 +77,13 @@ k_mx4_quantize_t(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t l
     uint4 v = make_uint4(0, 0, 0, 0);
     if (m0 + r < M && k0 + c < K)
       v = *reinterpret_cast<const uint4*>(src + (m0 + r) * ldx + k0 + c);
-    *reinterpret_cast<uint4*>(tile + r * kTK + c) = v;
+    *reinterpret_cast<uint4*>(tile + r * kTK + ((c + 16 * i) & (kTK - 1))) = v;
   }
   __syncthreads();
-  const int blk = tid >> 5, c = (tid & 31) * 2;
+  const int blk = tid & 7, c = (tid >> 3) * 2;
   if (m0 + 32 * blk >= M) return;          // M % 32 == 0: whole blocks
-  const uint32_t* col = reinterpret_cast<const uint32_t*>(tile + 32 * blk * kTK + c);
+  const uint32_t* col =
+      reinterpret_cast<const uint32_t*>(tile + 32 * blk * kTK + ((c + 16 * blk) & (kTK - 1)));
   uint32_t w[32];
   uint32_t lo = 0, hi = 0;
 #pragma unroll
