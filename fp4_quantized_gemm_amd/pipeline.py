@@ -196,6 +196,8 @@ def _check_block(x, logits, bias, w_first, w_down, train=False):
             _arg(w.codes, torch.uint8, name + "'s codes", dev, (E, N, K // 2))
             _arg(w.scales, torch.uint8, name + "'s scales", dev, (E, N, K // 32))
             if train:
+                # (the products take strided rows, the weight gradients do not)
+                _arg(x, torch.bfloat16, "x", dev, (T, H))
                 _arg(w.t_codes, torch.uint8, name + "'s transposed codes", dev, (E, K, N // 2))
                 _arg(w.t_scales, torch.uint8, name + "'s transposed scales", dev, (E, K, N // 32))
             continue
@@ -284,6 +286,8 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     T, H = st.topk_w.shape[0], _out_features(st.w_down)
     if getattr(d_out, "shape", None) != (T, H):
         raise NvfpError(f"d_out must be a device tensor of shape {[T, H]}")
+    if isinstance(st.w_down, MxWeights):                 # (whose products take strided rows)
+        _arg(d_out, torch.bfloat16, "d_out", d_out.device, (T, H))
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
     # which has twice the columns: it comes first)

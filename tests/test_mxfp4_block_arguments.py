@@ -95,6 +95,22 @@ def test_gradients_to_add_to_fit(made):
                                 dw_down=there(E, H, I, dtype=F32))
 
 
+def test_training_refuses_strided_rows_at_once(made):
+    """The products would take them, the weight gradients after them not: then
+    the first gradient would have been added to."""
+    wide = there(T, 2 * H)[:, :H]
+    with pytest.raises(F.NvfpError):
+        forward(True, x=wide)
+    assert not made
+    forward(False, x=wide)
+    st = forward(True)[1]
+    made.clear()
+    for bad in (wide, there(T, H, dtype=F32)):
+        with pytest.raises(F.NvfpError):
+            pipeline.moe_train_backward(st, bad, dw_first=there(E, 2 * I, H, dtype=F32))
+    assert not made
+
+
 def test_prepared_weights_are_stacked():
     for w in (there(4, 128), there(2, 4, 128, dtype=F32), torch.zeros(2, 4, 128, dtype=BF16), None):
         with pytest.raises(F.NvfpError):
