@@ -36,7 +36,7 @@ __device__ __forceinline__ uint32_t mx4_encode8(const uint4& v, uint32_t& sbyte)
 }
 
 // One lane per 8 columns, one pass: 2 bytes read and 0.53 written per
-// element.  IT: index type of the flat chunk number.
+// element.  Bound by memory: 16384x4096 33 us = 5.2 TB/s.  IT: index type of the flat chunk number.
 template <typename IT>
 __global__ void __launch_bounds__(256)
 k_mx4_quantize(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
@@ -62,6 +62,8 @@ k_mx4_quantize(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t ldx
 // columns of one block of 32 rows, and the 8 lanes of a column's 8 blocks write
 // 128 contiguous bytes of codes.  (A block's rows are rotated by 8 dwords more
 // than those of the block before: the lanes of a read take every bank alike.)
+// 128 matrices of 2048x768: 113 us = 4.5 TB/s; with a wave on two blocks of 64
+// columns, 32 contiguous bytes at a time, 132.
 constexpr int kTM = 256, kTK = 64;
 __global__ void __launch_bounds__(256)
 k_mx4_quantize_t(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t ldx,
@@ -115,7 +117,8 @@ k_mx4_quantize_t(const uint16_t* __restrict__ x, int64_t M, int64_t K, int64_t l
   }
 }
 
-// one lane per 8 elements: exact products (2 significant bits), no rounding
+// one lane per 8 elements: exact products (2 significant bits), no rounding;
+// 16384x4096 25 us
 template <typename IT>
 __global__ void __launch_bounds__(256)
 k_mx4_restore(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t M,

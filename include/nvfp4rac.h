@@ -466,8 +466,8 @@ int grouped_wgrad(const void* dy, const int32_t* dy_rows, int64_t M_dy, const vo
  *   hw[p] = w gate s up                  bf16 [T*tk][I] or NULL (the x of the
  *           down product's grouped_wgrad, whose dy is d_out itself)
  *   d_topk_w[t][j] = sum_i dh_i gate_i s_i up_i   float32 [T][tk] or NULL
- * The gradient of the routing logits follows from d_topk_w as that of a
- * softmax over the tk chosen experts.  inv_perm is a permutation; an entry
+ * The gradient of the routing logits follows from d_topk_w
+ * (moe_permute_backward).  inv_perm is a permutation; an entry
  * outside [0, T*tk) is skipped: its d_topk_w, and the rows that no entry
  * names, are left as they were.  No output overlaps an input.  Requires
  * 1 <= tk <= 32, T*tk < 2^31, I % 8 == 0 (I % 32 == 0 with y_scales),
