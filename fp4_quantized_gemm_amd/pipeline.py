@@ -135,6 +135,9 @@ def moe_forward_mxfp4(x, logits, topk, w_first: MxWeights, w_down: MxWeights, bi
     bf16, logits [T][E] f32, w_first [E][2I][H] (gate rows, then up rows),
     w_down [E][H][I] -> (out [T][H] bf16, dict: with keep=True every
     intermediate).  H and I multiples of 128."""
+    for name, w in (("w_first", w_first), ("w_down", w_down)):
+        if not isinstance(w, MxWeights):
+            raise NvfpError(f"{name} must be MxWeights (prepare_mxfp4_weights)")
     _check_block(x, logits, bias, w_first, w_down)
     with _where(x):
         ids, tw, offs, perm, inv = moe_permute(logits, topk, bias)
