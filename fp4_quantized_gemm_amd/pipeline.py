@@ -26,7 +26,7 @@ from . import (NvfpError, _arg, _wshape, grouped_mxfp4_gemm, grouped_mxfp4_gemm_
                grouped_w4a4_gemm_rac_per_expert, grouped_w4a4_gemm_rac_swiglu, grouped_wgrad,
                moe_permute, moe_permute_backward, moe_swiglu_backward, mxfp4_quantize, mxfp8_checkpoint,
                nvfp4_quantize_act_amax,
-               moe_unpermute_combine, nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act,
+               moe_unpermute_combine, moe_unpermute_combine_backward, nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act,
                select_residual_channels, select_residual_channels_per_expert)
 
 
@@ -166,6 +166,7 @@ class TrainState:
     w_first: QuantWeights
     w_down: QuantWeights
     has_bias: bool = False
+    y2: torch.Tensor = None  # the down projection's output by permuted row, if asked for
 
 
 def _out_features(w):
@@ -241,7 +242,7 @@ def _dgrad(d, rows, w, offs, M_total):
 
 
 def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeights, bias=None,
-                      checkpoint="mxfp8"):
+                      checkpoint="mxfp8", keep_y2=False):
     """The block with the trainer's W4A16 products (bf16 activations): x [T][H]
     bf16, logits [T][E] f32, w_first [E][2I][H], w_down [E][H][I] -> (out
     [T][H] bf16, TrainState).  With MxWeights (both, with their transposes; H
@@ -253,15 +254,17 @@ def moe_train_forward(x, logits, topk, w_first: QuantWeights, w_down: QuantWeigh
     block of 32, those under 2^-13 of its largest by more), which moves
     gradients of random data by 3 to 4% in norm.  "bf16" keeps them as they
     are, x itself and not a copy: it is not to be overwritten before the
-    backward pass."""
+    backward pass.  keep_y2=True keeps the down projection's output too, 2
+    bytes for each of its T*tk*H elements: d_topk_w is then the gradient of out
+    (see moe_train_backward)."""
     if checkpoint not in ("mxfp8", "bf16"):
         raise ValueError(f"checkpoint must be 'mxfp8' or 'bf16', not {checkpoint!r}")
     _check_block(x, logits, bias, w_first, w_down, train=True)
     with _where(x):
-        return _train_forward(x, logits, topk, w_first, w_down, bias, checkpoint == "mxfp8")
+        return _train_forward(x, logits, topk, w_first, w_down, bias, checkpoint == "mxfp8", keep_y2)
 
 
-def _train_forward(x, logits, topk, w_first, w_down, bias, mx):
+def _train_forward(x, logits, topk, w_first, w_down, bias, mx, keep_y2):
     ids, tw, offs, perm, inv = moe_permute(logits, topk, bias)
     rows = perm.numel()
     y1 = _product(x, perm, w_first, offs, rows)
@@ -273,7 +276,7 @@ def _train_forward(x, logits, topk, w_first, w_down, bias, mx):
         c0 = mxfp8_checkpoint(x)
         kept_x, x_scales, kept_y, y_scales = c0["codes"], c0["scales"], c1["codes"], c1["scales"]
     return out, TrainState(kept_x, x_scales, kept_y, y_scales, ids, tw, offs, perm, inv, w_first,
-                           w_down, bias is not None)
+                           w_down, bias is not None, y2 if keep_y2 else None)
 
 
 def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=None, dw_down=None,
@@ -284,12 +287,22 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
     the weight gradients are added to (gradient accumulation).  want_d_logits:
     also d_logits [T][E] f32 and, if the block had a bias, d_bias [E] f32.  The routing
     weight enters in the SwiGLU's backward pass, so d_out goes into both of the
-    down projection's products as it is, gathered by token."""
+    down projection's products as it is, gathered by token.
+
+    d_topk_w, and with it d_logits and d_bias, is <dh, h> of the backward pass's
+    own dh = W_down^T d_out and h.  out's gradient is <d_out, y2>; with W4A16
+    products the two differ by the rounding of dh and the checkpoint of h.  With
+    MXFP4 they do not take the same operands (d_out and the weights' transposes
+    are rounded to 4 bits in the one, h and the weights in the other), and
+    <dh, h> is 15 to 19% in norm off <d_out, y2> for random data (of the block
+    without any rounding both are about as far, 27 and 29%, like dx, 29%).  The
+    state of keep_y2=True has y2, and d_topk_w is <d_out, y2>."""
     # (d_out is gathered by token, a token past its end as its last row)
     T, H = st.topk_w.shape[0], _out_features(st.w_down)
     if getattr(d_out, "shape", None) != (T, H):
         raise NvfpError(f"d_out must be a device tensor of shape {[T, H]}")
-    if isinstance(st.w_down, MxWeights):                 # (whose products take strided rows)
+    # (MXFP4 products take strided rows, the weight gradients and y2's not)
+    if isinstance(st.w_down, MxWeights) or st.y2 is not None:
         _arg(d_out, torch.bfloat16, "d_out", d_out.device, (T, H))
     # all that the weight gradients could refuse, before one of them has been
     # added to (their own limits are the stricter for the first product's,
@@ -311,8 +324,14 @@ def moe_train_backward(st: TrainState, d_out, dw_dtype=torch.float32, dw_first=N
 def _train_backward(st, d_out, dw_dtype, dw_first, dw_down, want_d_logits):
     acc1, acc2 = dw_first is not None, dw_down is not None
     rows = st.perm_token.numel()
+    exact_tw = None
+    if st.y2 is not None:
+        # (y2's own gradient, w d_out by row, is not used: the products take d_out)
+        exact_tw = moe_unpermute_combine_backward(d_out, st.y2, st.inv_perm, st.topk_w)[1]
     dh = _dgrad(d_out, st.perm_token, st.w_down, st.offsets, rows)
     dy1, hw, d_tw = moe_swiglu_backward(st.y1, dh, st.inv_perm, st.topk_w, y_scales=st.y1_scales)
+    if exact_tw is not None:
+        d_tw = exact_tw
     g_first = grouped_wgrad(dy1, None, st.x, st.perm_token, st.offsets, x_scales=st.x_scales,
                             M_total=rows, dtype=dw_dtype, out=dw_first, accumulate=acc1)
     g_down = grouped_wgrad(d_out, st.perm_token, hw, None, st.offsets, M_total=rows,

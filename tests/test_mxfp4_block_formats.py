@@ -22,3 +22,28 @@ def test_serving_takes_mxfp4_weights_only(made, first, down):  # noqa: F811
     assert not made
     forward(False)
     assert made
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_calls_of_a_step_that_keeps_y2(made, monkeypatch, keep):  # noqa: F811
+    """y2's gradient is taken before any weight gradient is added to, and d_topk_w
+    and the logits' gradient are formed from its result."""
+    exact, seen = there(T, TK, dtype=F32), []
+    monkeypatch.setattr(pipeline, "moe_unpermute_combine_backward",
+                        lambda *a: made.append(("combine_backward", {})) or (None, exact))
+    route = pipeline.moe_permute_backward
+    monkeypatch.setattr(pipeline, "moe_permute_backward", lambda *a, **kw: seen.append(a[2]) or route(*a, **kw))
+    args = (there(T, H), there(T, E, dtype=F32), TK, mx(E, 2 * I, H), mx(E, H, I))
+    st = pipeline.moe_train_forward(*args, keep_y2=keep)[1]
+    assert (st.y2 is not None) == keep
+    made.clear()
+    g = pipeline.moe_train_backward(st, there(T, H), want_d_logits=True)
+    names = [n for n, _ in made]
+    assert ("combine_backward" in names) == keep and (g["d_topk_w"] is exact) == keep
+    assert (seen[0] is exact) == keep
+    if keep:
+        assert names.index("combine_backward") < names.index("grouped_wgrad")
+    made.clear()
+    with pytest.raises(F.NvfpError):
+        pipeline.moe_train_backward(st, there(T, 2 * H)[:, :H])
+    assert not made
