@@ -272,6 +272,14 @@ __device__ __forceinline__ void mx_wait() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | (7 << 4));
   asm volatile("" ::: "memory");
 }
+// all but the newest N of the wave's reads and writes of LDS are done (they
+// end in the order in which they were issued)
+template <int N>
+__device__ __forceinline__ void mx_wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (N << 8));
+  asm volatile("" ::: "memory");
+}
 __device__ __forceinline__ void mx_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -576,6 +584,7 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
         }
         uint32_t here = (uint32_t)(r32 * 128 + (((HALF ? 2 * q : 4 * q) ^ ((r32 >> 1) & 7)) << 4));
         asm volatile("" : "+v"(here));                   // (its sums are not kept in registers)
+        if constexpr (!LAST) issue_a(other, kt + 1);
         u32x4 W[S][2], A[S][NV];
         auto read_a = [&](int s) {
 #pragma unroll
@@ -585,13 +594,16 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i) W[s][i] = ld(sw, (here ^ (16u * s)) + (uint32_t)(8192 * wave) + 4096u * i);
+        // (the reads of the scales and the weights are issued before this, at least
+        // the 2 NV of A[0] and A[1] after it)
+        asm volatile("" ::: "memory");
         read_a(0);
         const bool ahead = !LAST || more;
         if (LAST && more) {
           aim(nxt, rows[buf ^ 1]);
           if (taken && tid == 0) next_v = first + 2 * stride + ticket;
+          issue_a(other, 0);
         }
-        if (ahead) issue_a(other, LAST ? 0 : kt + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -607,9 +619,12 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
             }
           __builtin_amdgcn_sched_barrier(0);
           if (s == 0 && ahead) {
-            // the first products waited for the last of the weights' reads:
-            // their stage is free.  The scales' is one step later, or once every
-            // wave has read the tile's last.
+            // Every read of the weights' stage, which only this wave reads, is done:
+            // it is free.  (A wait of its own: the products above would wait for
+            // it too, but the compiler may move them behind these loads.)  The
+            // scales' stage is free one step later, or once every wave has read
+            // the tile's last.
+            mx_wait_lds<NV>();
             issue_w(LAST ? 0 : kt + 1);
             if (U == 1 || LAST) {
               if (U == 0) mx_barrier();
