@@ -689,15 +689,22 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
               *reinterpret_cast<uint2*>(own + (r * (16 * LR) + (piece << 4) + half * 8)) =
                   make_uint2(u[0], u[1]);
             }
-          // (other lanes have written what is read next)
+          // (other lanes have written what is read next, and write over it for the
+          // next 32 rows: a wave's accesses of LDS end in their order)
+          asm volatile("" ::: "memory");
+          u32x4 h[LR / 2];
+#pragma unroll
+          for (int t = 0; t < LR / 2; ++t) {
+            const int row = (64 / LR) * t + l / LR, c = l % LR;
+            h[t] = *reinterpret_cast<const u32x4*>(
+                own + (row * (16 * LR) + ((GLU ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7)) << 4)));
+          }
           asm volatile("" ::: "memory");
 #pragma unroll
           for (int t = 0; t < LR / 2; ++t) {
             const int row = (64 / LR) * t + l / LR, c = l % LR;
-            const u32x4 h = *reinterpret_cast<const u32x4*>(
-                own + (row * (16 * LR) + ((GLU ? c ^ ((row >> 2) & 3) : c ^ ((row >> 1) & 7)) << 4)));
             // (rows 16 .. 31, the second half of the reads, have their halves swapped)
-            const u32x4 o = t < LR / 4 ? h : u32x4{h.z, h.w, h.x, h.y};
+            const u32x4 o = t < LR / 4 ? h[t] : u32x4{h[t].z, h[t].w, h[t].x, h[t].y};
             const uint32_t n = n0 + 8 * c;
             __builtin_amdgcn_raw_buffer_store_b128(
                 o, rs_y, n < NO ? ((uint32_t)(32 * j + row) * NO + n) * 2u : 0xFFFFFFF0u, 0, 2);
