@@ -370,7 +370,10 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
   // separate objects, each access naming its own: the compiler then does not
   // wait for loads into the others
   __shared__ __attribute__((aligned(16))) uint8_t sa0[A_BYTES], sa1[A_BYTES], sw[W_BYTES], ssc[SCALES];
-  __shared__ int32_t rows[2][BM], prefix[1025], next_v;
+  __shared__ int32_t rows[2][BM], prefix[1025];
+  // written by one wave and read by all, once per tile, so by atomics: no plain
+  // read of it may be taken out of the loop, whatever fences are there
+  __shared__ int32_t next_v;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -601,7 +604,8 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
         const bool ahead = !LAST || more;
         if (LAST && more) {
           aim(nxt, rows[buf ^ 1]);
-          if (taken && tid == 0) next_v = first + 2 * stride + ticket;
+          if (taken && tid == 0)
+            __hip_atomic_store(&next_v, first + 2 * stride + ticket, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
           issue_a(other, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -716,8 +720,7 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
     };
     using n4 = std::integral_constant<int, 4>;
     using n2 = std::integral_constant<int, 2>;
-    // (as functions of their own these would have their captures in memory, and
-    // next_v's read was then taken out of the loop that it ends)
+    // (as functions of their own these would have their captures in memory)
     auto tile = [&](uint8_t* const x, uint8_t* const y) __attribute__((always_inline)) {
       if (cur.valid > 64) run(n4{}, x, y);
       else run(n2{}, x, y);
@@ -725,8 +728,10 @@ k_mx_big(MxGemmArgs p, int32_t* __restrict__ taken, int max_m, int n_tiles) {
     if (kOdd && odd) tile(sa1, sa0);
     else tile(sa0, sa1);
     if (!more) return;
-    asm volatile("" ::: "memory");                     // (read here, once per tile)
-    v = taken ? __builtin_amdgcn_readfirstlane(next_v) : v + stride;
+    if (taken)
+      v = __builtin_amdgcn_readfirstlane(__hip_atomic_load(&next_v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP));
+    else
+      v += stride;
     cur = nxt;
     buf ^= 1;
     odd = !odd;
