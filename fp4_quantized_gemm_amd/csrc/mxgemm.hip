@@ -317,7 +317,7 @@ __device__ __forceinline__ void mx_count_tiles(const MxGemmArgs& p, int cap, int
   for (int i = 0; i < 4; ++i) {
     int lo = off[i], hi = off[i + 1];
     clamp_rows((int)p.M_total, lo, hi);
-    n[i] = 4 * tid + i < p.E ? (int)((uint32_t)(hi - lo + mxb::BM - 1) / mxb::BM) : 0;
+    n[i] = 4 * tid + i < p.E ? (int)(((uint32_t)(hi - lo) + (mxb::BM - 1)) / mxb::BM) : 0;
     sum = min(sum + n[i], cap);
   }
   int incl = sum;
