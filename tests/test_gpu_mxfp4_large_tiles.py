@@ -1,6 +1,7 @@
 """The edges of grouped_mxfp4_gemm's large tiles: NaN scales, rows out of range,
-memory that is aligned to 4 bytes only, column tiles that end early.  Every case
-asserts that the call's rule sends it to that kernel.
+memory that is aligned to 4 bytes only, column tiles that end early, counters
+in replayed graphs and on two streams.  Every case asserts that the call's rule
+sends it to that kernel, and where counters matter, that they are used.
 
 Tolerances as in test_gpu_mxfp4.py: a sum of K exact products is off by at most
 K 2^-23 of the sum of magnitudes, the output's rounding by 2^-8 of its value."""
@@ -25,6 +26,13 @@ def is_large(P, E, N, glu):
     """More than 512 tiles of 16 rows x 64 columns, by the call's estimate."""
     active = min(P, E)
     return up(N // 2 if glu else N, 64) * max(up(P, 16) + active // 2, active) > 512
+
+
+def is_counted(P, E, N, K):
+    """More than 72 steps of K for a workgroup: tiles taken as they get free."""
+    tiles = (up(P, 128) + E) * up(N, 256)
+    groups = min(up(tiles, 8) * 8, up(2 * torch.cuda.get_device_properties(0).multi_processor_count, 8) * 8)
+    return tiles * up(K, 256) > 72 * groups
 
 
 # K / 128 modulo 4 from 0 to 3, rows of scales shorter than 16 bytes among them
@@ -149,3 +157,62 @@ def test_column_tiles_that_end_early(dev, N, K, glu):
         lim = d + 2.0 ** -8 * (y.abs() + d) + 2.0 ** -120
         off = (got[lo:hi].double() - y).abs()
         assert bool((off <= lim).all()), (e, int((off > lim).sum()))
+
+
+# ---------------------------------------------------------------- counters
+COUNTED = dict(counts=[3000, 1, 70, 2500, 0, 130], N=12288, K=4096)
+
+
+def counted_set(seed, gather):
+    counts, N, K = COUNTED["counts"], COUNTED["N"], COUNTED["K"]
+    P, E = sum(counts), len(counts)
+    assert is_large(P, E, N, True) and is_counted(P, E, N, K)
+    g = torch.Generator("cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)     # noqa: E731
+    M_src = 4000 if gather else P
+    rows = torch.randint(0, M_src, (P,), generator=g, device="cuda", dtype=torch.int32) if gather else None
+    return [*F.mxfp4_quantize(rand(M_src, K)), rows, *F.mxfp4_quantize(rand(E, N, K)), cu(offsets_of(counts))]
+
+
+@pytest.mark.parametrize("glu", [False, True])
+def test_counters_in_replayed_graphs(dev, glu):
+    """Two graphs of the same call, replayed several times with eager calls
+    between, also for other rows and offsets in place: every replay has to find
+    its counters at nought."""
+    say(f"large tiles graphs glu={glu}")
+    s = counted_set(5, True)
+    CALLS[glu](*s)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = CALLS[glu](*s)
+        graphs.append((g, got))
+    for i in range(5):
+        if i == 3:
+            s[2].copy_(s[2].flip(0))
+            s[5].copy_(cu(offsets_of([100, 2900, 1, 70, 2600, 30])))
+        want = CALLS[glu](*s).clone()
+        for _, got in graphs:
+            got.zero_()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(same(got, want) for _, got in graphs), f"replay {i}"
+
+
+def test_counters_on_two_streams(dev):
+    """Calls on two streams at once, each with its own counters."""
+    say("large tiles streams")
+    sets = [counted_set(7, True), counted_set(8, False)]
+    want = [CALLS[glu](*s) for s in sets for glu in (False, True)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(4):
+        got = []
+        for s, q in zip(sets, streams):
+            with torch.cuda.stream(q):
+                got += [CALLS[glu](*s) for glu in (False, True)]
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want)), i
