@@ -227,18 +227,19 @@ k_mx_few(MxGemmArgs p) {
 // empties into registers at the start of a step and fills again at once.
 //
 // A stage's row is its 128 code bytes, eight 16-byte pieces; piece c lies at
-// place c ^ ((row >> 1) & 7), so that the 32 rows of a fragment read without
-// bank conflicts.  Lane (r, q) of instruction s = 0 .. 3 takes piece 4 q + s of
-// its row, both operands alike: which 32 of the 256 columns a lane of an
-// instruction has does not matter for the sum, and so the scales of the four
-// are the bytes of one dword.  (A last step of 128 columns: s = 0, 1, piece
-// 2 q + s.)  Scales take the same way through LDS, 16 bytes of a row for two
-// steps.
+// place c ^ ((row >> 1) & 7), so that a fragment's 32 rows are spread over all
+// banks.  (The scales' are not: rows 16 bytes apart, two to a bank.  Counted over
+// the whole kernel, 29% of the cycles in which LDS is busy are conflicts.)  Lane
+// (r, q) of instruction s = 0 .. 3 takes piece 4 q + s of its row, both operands
+// alike: which 32 of the 256 columns a lane of an instruction has does not matter
+// for the sum, and so the scales of the four are the bytes of one dword.  (A last
+// step of 128 columns: s = 0, 1, piece 2 q + s.)  Scales take the same way
+// through LDS, 16 bytes of a row for two steps.
 //
-// Measured: 131072 rows over 128 experts of 4096x1536 556 us (2.97 PFLOP/s, 1.6
-// GB), 32768 skewed rows over 128 of 1536x2048 with SwiGLU 89 us, 2048 rows over
-// 128 of 4096x1536 86 us (4.9 TB/s of weights), one 8192x8192 with 16384 rows 545
-// us (4.0 PFLOP/s).  The first is bound by waits between loads, products and
+// Measured: 131072 rows over 128 experts of 4096x1536 552 to 563 us, by card (2.9
+// to 3.0 PFLOP/s, 1.6 GB), 32768 skewed rows over 128 of 1536x2048 with SwiGLU 89
+// us, 2048 rows over 128 of 4096x1536 86 us (4.9 TB/s of weights), one 8192x8192
+// with 16384 rows 545 us (4.0 PFLOP/s).  The first is bound by waits between loads, products and
 // stores at 1.9 GHz: the matrix units are 39% busy; of 580 us on another card,
 // 489 were left without the stores, 458 without the weights' loads, 338 for the
 // products and LDS reads alone; on codes of zeros, which draw less power, it

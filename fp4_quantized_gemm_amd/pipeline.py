@@ -22,7 +22,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (NvfpError, _arg, _wshape, grouped_mxfp4_gemm, grouped_mxfp4_gemm_swiglu, grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
+from . import (NvfpError, _arg, _wshape, grouped_mxfp4_gemm, grouped_mxfp4_gemm_swiglu,
+               grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
                grouped_w4a4_gemm_rac_per_expert, grouped_w4a4_gemm_rac_swiglu, grouped_wgrad,
                moe_permute, moe_permute_backward, moe_swiglu_backward, mxfp4_quantize, mxfp8_checkpoint,
                nvfp4_quantize_act_amax,
