@@ -25,9 +25,9 @@ import torch
 from . import (NvfpError, _arg, _wshape, grouped_mxfp4_gemm, grouped_mxfp4_gemm_swiglu,
                grouped_w4a16_dgrad, grouped_w4a16_gemm, grouped_w4a4_gemm_rac,
                grouped_w4a4_gemm_rac_per_expert, grouped_w4a4_gemm_rac_swiglu, grouped_wgrad,
-               moe_permute, moe_permute_backward, moe_swiglu_backward, mxfp4_quantize, mxfp8_checkpoint,
-               nvfp4_quantize_act_amax,
-               moe_unpermute_combine, moe_unpermute_combine_backward, nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act,
+               moe_permute, moe_permute_backward, moe_swiglu_backward, moe_unpermute_combine,
+               moe_unpermute_combine_backward, mxfp4_quantize, mxfp8_checkpoint,
+               nvfp4_qdq_residual, nvfp4_qdq_weights, nvfp4_quantize_act, nvfp4_quantize_act_amax,
                select_residual_channels, select_residual_channels_per_expert)
 
 
